@@ -6,7 +6,9 @@ memory and the current CUDA stream.  There is no fallback: if the library is
 missing or cannot be loaded, every call raises.
 
 The function names mirror the C entry points: ``fp4_quantize``,
-``fp4_gemm``, ``fqt_linear_fwd``, ``fqt_linear_bwd``.
+``fp4_gemm``, ``fqt_linear_fwd``, ``fqt_linear_bwd``; between two linears
+``fqt_rmsnorm_fwd/bwd``, ``fqt_act_fwd/bwd`` (with 8-bit checkpoints,
+``Ckpt8``) and ``fp4_gemm_epi``.
 """
 from __future__ import annotations
 
@@ -24,6 +26,8 @@ RTN, SR, QUEST = 0, 1, 2
 BLOCK_1D, BLOCK_2D = 0, 1
 OUT_BF16, OUT_F32 = 0, 1
 RHT_FPROP, RHT_DGRAD, RHT_WGRAD = 1, 2, 4
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
+RMS_Y, RMS_XHAT = 0, 1
 
 STATUS = {0: "FP4_OK", 1: "FP4_ERR_NULL", 2: "FP4_ERR_SHAPE", 3: "FP4_ERR_ALIGN",
           4: "FP4_ERR_FORMAT", 5: "FP4_ERR_WORKSPACE", 6: "FP4_ERR_CUDA",
@@ -34,7 +38,9 @@ EXPORTS = ("fp4_qtensor_sizes", "fp4_qparams_default", "fp4_workspace_bytes", "f
            "fp4_gemm", "fqt_linear_cfg_default", "fqt_linear_fwd", "fqt_linear_bwd",
            "fp4_read_device_status", "fp4_clear_device_status", "fp4_status_str",
            "fp4_abi_version", "fp4_kernel_launches", "fp4_gemm_noalloc", "fp4_mma_rate",
-           "fp4_quant_noise", "fp4_gemm_quant", "fp4_gemm_quant_ex", "fp4_allreduce_sum_f32")
+           "fp4_quant_noise", "fp4_gemm_quant", "fp4_gemm_quant_ex", "fp4_allreduce_sum_f32",
+           "fqt_ckpt8_sizes", "fqt_colsum_workspace_bytes", "fqt_rmsnorm_fwd", "fqt_rmsnorm_bwd",
+           "fqt_act_fwd", "fqt_act_bwd", "fp4_gemm_epi")
 
 
 class Fp4Error(RuntimeError):
@@ -65,6 +71,17 @@ class LinearCfgC(C.Structure):
 class SavedC(C.Structure):
     _fields_ = [("xq", QTensorC), ("xq_t", QTensorC), ("wq", QTensorC), ("wq_t", QTensorC),
                 ("dyq", QTensorC), ("dyq_t", QTensorC)]
+
+
+class Ckpt8C(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("rows", C.c_int64),
+                ("cols", C.c_int64)]
+
+
+class EpilogueC(C.Structure):
+    _fields_ = [("bias", C.c_void_p), ("residual", C.c_void_p), ("ld_residual", C.c_int64),
+                ("z8", C.POINTER(Ckpt8C)), ("act", C.c_int32), ("bias_dtype", C.c_int32),
+                ("residual_dtype", C.c_int32)]
 
 
 _lib = None
@@ -126,6 +143,24 @@ def load() -> C.CDLL:
     L.fp4_gemm_noalloc.restype = i32
     L.fp4_gemm_noalloc.argtypes = [C.POINTER(QTensorC), C.POINTER(QTensorC), C.c_float, vp, i64,
                                    i32, vp, vp]
+    f32, ck = C.c_float, C.POINTER(Ckpt8C)
+    L.fqt_ckpt8_sizes.restype = None
+    L.fqt_ckpt8_sizes.argtypes = [i64, i64, C.POINTER(sz), C.POINTER(sz)]
+    L.fqt_colsum_workspace_bytes.restype = sz
+    L.fqt_colsum_workspace_bytes.argtypes = [i64, i64]
+    L.fqt_rmsnorm_fwd.restype = i32
+    L.fqt_rmsnorm_fwd.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, i32, f32, i64, i64, vp, i64, ck,
+                                  i32, vp, vp, vp, sz, vp]
+    L.fqt_rmsnorm_bwd.restype = i32
+    L.fqt_rmsnorm_bwd.argtypes = [vp, i64, vp, i64, i32, ck, vp, vp, i32, vp, i64, vp, i64, i32, i64,
+                                  i64, vp, vp, sz, vp]
+    L.fqt_act_fwd.restype = i32
+    L.fqt_act_fwd.argtypes = [vp, i64, ck, i32, i32, i64, i64, vp, i64, ck, vp, vp, sz, vp]
+    L.fqt_act_bwd.restype = i32
+    L.fqt_act_bwd.argtypes = [vp, i64, vp, i64, ck, i32, i32, i64, i64, vp, i64, vp, vp, vp, sz, vp]
+    L.fp4_gemm_epi.restype = i32
+    L.fp4_gemm_epi.argtypes = [C.POINTER(QTensorC), C.POINTER(QTensorC), f32, C.POINTER(EpilogueC), vp,
+                               i64, i32, vp, vp, sz, vp]
     _lib = L
     return L
 
@@ -202,6 +237,16 @@ class Workspace:
     def __init__(self, M: int = 128, N: int = 128, K: int = 64, device="cuda"):
         n = load().fp4_workspace_bytes(M, N, K)
         self.buf = torch.zeros(n, dtype=torch.uint8, device=device)
+
+    @staticmethod
+    def colsum(rows: int, cols: int, device="cuda") -> "Workspace":
+        """A workspace of the calls that sum over the rows of a [rows, cols]
+        tensor (dweight, dbias); good for every other call too."""
+        w = Workspace.__new__(Workspace)
+        n = max(load().fqt_colsum_workspace_bytes(rows, cols), load().fp4_workspace_bytes(128, 128, 64))
+        w.buf = torch.empty(n, dtype=torch.uint8, device=device)
+        w.buf[:256].zero_()
+        return w
 
     @property
     def ptr(self):
@@ -403,3 +448,234 @@ def fqt_linear_bwd(cfg: LinearCfgC, dy: torch.Tensor, saved: Saved, dx: torch.Te
     code = load().fqt_linear_bwd(C.byref(cfg), M, N, K, _ptr(dy), C.byref(saved._c), _ptr(dx),
                                  _ptr(dw), ws.ptr, ws.nbytes, _stream(stream))
     _check(code, "fqt_linear_bwd")
+
+
+# --------------------------------------------------------------------------
+# Between two linears: RMS norm, activations, the GEMM with an epilogue, and
+# 8-bit checkpoints.  The library sees pointers and sizes, so each tensor's
+# type, shape and device is checked here, before the call.
+# --------------------------------------------------------------------------
+@dataclass
+class Ckpt8:
+    """An 8-bit checkpoint of a [rows, cols] tensor: E4M3 codes [rows, cols]
+    and one E8M0 scale per 32 columns, scales [rows, cols // 32] (both as
+    bytes; views as torch.float8_e4m3fn / torch.float8_e8m0fnu are their
+    values)."""
+    rows: int
+    cols: int
+    codes: torch.Tensor
+    scales: torch.Tensor
+    _c: Ckpt8C = field(default=None, repr=False)
+
+    @staticmethod
+    def empty(rows: int, cols: int, device="cuda") -> "Ckpt8":
+        if rows < 0 or cols <= 0 or cols % 32:
+            raise ValueError(f"Ckpt8: cols must be a positive multiple of 32, got [{rows}, {cols}]")
+        dev = torch.device(device)
+        codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+        scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
+        return Ckpt8(rows, cols, codes, scales,
+                     Ckpt8C(codes.data_ptr(), scales.data_ptr(), rows, cols))
+
+
+_FLOATS = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
+
+
+def _bad(where, name, t, want):
+    got = f"{tuple(t.shape)} {t.dtype} {t.device}" if isinstance(t, torch.Tensor) else repr(t)
+    raise ValueError(f"{where}: {name} must be {want}, got {got}")
+
+
+def _mat(where, name, t, rows, cols, device, types=(torch.bfloat16,)):
+    """Pointer and leading dimension of a [rows, cols] matrix, (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or t.dtype not in types or \
+            t.device != device or (t.stride(1) != 1 and cols > 1):
+        _bad(where, name, t, f"a [{rows}, {cols}] row-major matrix of {types} on {device}")
+    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+
+
+def _vec(where, name, t, n, device, types=(torch.float32,)):
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != n or t.dtype not in types or t.device != device or \
+            not t.is_contiguous():
+        _bad(where, name, t, f"a dense vector of {n} {types} on {device}")
+    return t.data_ptr()
+
+
+def _ckpt(where, name, q, rows, cols, device):
+    if q is None:
+        return None
+    if not isinstance(q, Ckpt8) or q.rows != rows or q.cols != cols or q.codes.device != device:
+        _bad(where, name, q, f"a Ckpt8 of [{rows}, {cols}] on {device}")
+    return C.byref(q._c)
+
+
+def _work(where, ws, device):
+    if ws is None:
+        return None, 0
+    if ws.buf.device != device:
+        _bad(where, "ws", ws.buf, f"a workspace on {device}")
+    return ws.buf.data_ptr(), ws.buf.numel()
+
+
+def _on_device(where, device, stream):
+    """The stream's handle, with `device` checked to be the current device:
+    kernels launch on the current one."""
+    if device.type != "cuda":
+        raise ValueError(f"{where}: tensors must be on a CUDA device, got {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: tensors are on {device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()} (use torch.cuda.device)")
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    if stream.device != device:
+        raise ValueError(f"{where}: stream of {stream.device}, tensors on {device}")
+    return stream.cuda_stream
+
+
+def fqt_rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor | None = None,
+                    residual: torch.Tensor | None = None, res_out: torch.Tensor | None = None,
+                    q8: Ckpt8 | None = None, q8_of: int = RMS_Y, rstd: torch.Tensor | None = None,
+                    y_amax: torch.Tensor | None = None, eps: float = 1e-6,
+                    ws: Workspace | None = None, stream=None):
+    """s = x + residual -> res_out; rstd = (mean s^2 + eps)^-1/2; y = s * rstd * weight.
+    q8 receives the 8-bit form of y (RMS_Y) or of s * rstd (RMS_XHAT, what
+    fqt_rmsnorm_bwd takes).  x, y BF16; residual and res_out both BF16 or both
+    FP32 (res_out may be residual); weight BF16 or FP32."""
+    me, dev = "fqt_rmsnorm_fwd", x.device
+    if x.dim() != 2:
+        _bad(me, "x", x, "a matrix")
+    rows, cols = x.shape
+    xp, ldx = _mat(me, "x", x, rows, cols, dev)
+    rp, ldr = _mat(me, "residual", residual, rows, cols, dev, _FLOATS)
+    op, ldo = _mat(me, "res_out", res_out, rows, cols, dev, _FLOATS)
+    if (residual is None) != (res_out is None) or (residual is not None and
+                                                   residual.dtype != res_out.dtype):
+        raise ValueError(f"{me}: residual and res_out go together and have one type")
+    yp, ldy = _mat(me, "y", y, rows, cols, dev)
+    wp = _vec(me, "weight", weight, cols, dev, _FLOATS)
+    wsp, wsn = _work(me, ws, dev)
+    h = _on_device(me, dev, stream)
+    _check(load().fqt_rmsnorm_fwd(
+        xp, ldx, rp, ldr, op, ldo, OUT_BF16 if residual is None else _FLOATS[residual.dtype], wp,
+        _FLOATS[weight.dtype], eps, rows, cols, yp, ldy, _ckpt(me, "q8", q8, rows, cols, dev), q8_of,
+        _vec(me, "rstd", rstd, rows, dev), _vec(me, "y_amax", y_amax, 1, dev), wsp, wsn, h), me)
+
+
+def fqt_rmsnorm_bwd(dy: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, dx: torch.Tensor,
+                    s: torch.Tensor | None = None, xhat8: Ckpt8 | None = None,
+                    dres: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
+                    ws: Workspace | None = None, stream=None):
+    """dx = rstd * (g - xhat * mean(g * xhat)) + dres with g = dy * weight, and
+    dweight = sum over rows of dy * xhat (FP32).  xhat comes from the 8-bit
+    checkpoint `xhat8` or as s * rstd.  dres and dx have one type, BF16 or
+    FP32 (dx may be dres).  With dweight, ws is Workspace.colsum(rows, cols)
+    (made here when None)."""
+    me, dev = "fqt_rmsnorm_bwd", dy.device
+    if dy.dim() != 2:
+        _bad(me, "dy", dy, "a matrix")
+    rows, cols = dy.shape
+    if (s is None) == (xhat8 is None):
+        raise ValueError(f"{me}: exactly one of s and xhat8")
+    dyp, lddy = _mat(me, "dy", dy, rows, cols, dev)
+    sp, lds = _mat(me, "s", s, rows, cols, dev, _FLOATS)
+    drp, lddr = _mat(me, "dres", dres, rows, cols, dev, _FLOATS)
+    dxp, lddx = _mat(me, "dx", dx, rows, cols, dev, _FLOATS)
+    if dres is not None and dres.dtype != dx.dtype:
+        raise ValueError(f"{me}: dres and dx have one type")
+    wp = _vec(me, "weight", weight, cols, dev, _FLOATS)
+    if dweight is not None and ws is None:
+        ws = Workspace.colsum(rows, cols, device=dev)
+    wsp, wsn = _work(me, ws, dev)
+    h = _on_device(me, dev, stream)
+    _check(load().fqt_rmsnorm_bwd(
+        dyp, lddy, sp, lds, OUT_BF16 if s is None else _FLOATS[s.dtype],
+        _ckpt(me, "xhat8", xhat8, rows, cols, dev), _vec(me, "rstd", rstd, rows, dev), wp,
+        _FLOATS[weight.dtype], drp, lddr, dxp, lddx, _FLOATS[dx.dtype], rows, cols,
+        _vec(me, "dweight", dweight, cols, dev), wsp, wsn, h), me)
+
+
+def _z(me, z, rows, zcols, dev):
+    """(pointer, leading dimension, checkpoint) of a z given as a matrix or a Ckpt8."""
+    if isinstance(z, Ckpt8):
+        return None, 0, _ckpt(me, "z", z, rows, zcols, dev)
+    zp, ldz = _mat(me, "z", z, rows, zcols, dev)
+    return zp, ldz, None
+
+
+def fqt_act_fwd(z, y: torch.Tensor | None = None, act: int = ACT_SILU, gated: bool = False,
+                z8: Ckpt8 | None = None, y_amax: torch.Tensor | None = None,
+                ws: Workspace | None = None, stream=None):
+    """y = act(z), or act(z[:, :F]) * z[:, F:] with gated (z [rows, 2 F]).  z is a
+    BF16 matrix, or a Ckpt8 (recomputation; with ACT_NONE its decoding).  z8
+    receives the 8-bit checkpoint of a matrix z (y None: encoding alone)."""
+    me = "fqt_act_fwd"
+    src = z.codes if isinstance(z, Ckpt8) else z
+    dev = src.device
+    if src.dim() != 2 or (gated and src.shape[1] % 2):
+        _bad(me, "z", src, "a matrix, with an even row length when gated")
+    rows, zcols = src.shape
+    cols = zcols // 2 if gated else zcols
+    zp, ldz, zc = _z(me, z, rows, zcols, dev)
+    yp, ldy = _mat(me, "y", y, rows, cols, dev)
+    wsp, wsn = _work(me, ws, dev)
+    h = _on_device(me, dev, stream)
+    _check(load().fqt_act_fwd(zp, ldz, zc, act, 1 if gated else 0, rows, cols, yp, ldy,
+                              _ckpt(me, "z8", z8, rows, zcols, dev),
+                              _vec(me, "y_amax", y_amax, 1, dev), wsp, wsn, h), me)
+
+
+def fqt_act_bwd(dy: torch.Tensor, z, dz: torch.Tensor, act: int = ACT_SILU, gated: bool = False,
+                dbias: torch.Tensor | None = None, dz_amax: torch.Tensor | None = None,
+                ws: Workspace | None = None, stream=None):
+    """dz from dy and z (a BF16 matrix or a Ckpt8): dy * act'(z), or with gated
+    [dy * z[:, F:] * act'(z[:, :F]), dy * act(z[:, :F])].  dbias (FP32): sums of dz
+    over the rows; ws is then Workspace.colsum(rows, z's row length) (made here
+    when None)."""
+    me, dev = "fqt_act_bwd", dy.device
+    if dy.dim() != 2:
+        _bad(me, "dy", dy, "a matrix")
+    rows, cols = dy.shape
+    zcols = 2 * cols if gated else cols
+    dyp, lddy = _mat(me, "dy", dy, rows, cols, dev)
+    zp, ldz, zc = _z(me, z, rows, zcols, dev)
+    dzp, lddz = _mat(me, "dz", dz, rows, zcols, dev)
+    if dbias is not None and ws is None:
+        ws = Workspace.colsum(rows, zcols, device=dev)
+    wsp, wsn = _work(me, ws, dev)
+    h = _on_device(me, dev, stream)
+    _check(load().fqt_act_bwd(dyp, lddy, zp, ldz, zc, act, 1 if gated else 0, rows, cols, dzp, lddz,
+                              _vec(me, "dbias", dbias, zcols, dev),
+                              _vec(me, "dz_amax", dz_amax, 1, dev), wsp, wsn, h), me)
+
+
+def fp4_gemm_epi(a: QTensor, b: QTensor, out: torch.Tensor, alpha: float = 1.0,
+                 bias: torch.Tensor | None = None, act: int = ACT_NONE,
+                 residual: torch.Tensor | None = None, z8: Ckpt8 | None = None,
+                 c_amax: torch.Tensor | None = None, ws: Workspace | None = None, stream=None):
+    """out = act(z) + residual with z = (fp4_gemm's FP32 result) + bias; z8 receives
+    the 8-bit checkpoint of z.  bias [N] and residual [M, N] BF16 or FP32
+    (residual may be out itself)."""
+    me, dev = "fp4_gemm_epi", out.device
+    M, N = a.rows, b.rows
+    for name, q in (("a", a), ("b", b)):
+        if q.codes.device != dev:
+            _bad(me, name, q.codes, f"an operand on {dev}")
+    cp, ldc = _mat(me, "out", out, M, N, dev, _FLOATS)
+    rp, ldr = _mat(me, "residual", residual, M, N, dev, _FLOATS)
+    if ws is None:
+        ws = Workspace(M, N, a.cols, device=dev)
+    wsp, wsn = _work(me, ws, dev)
+    if z8 is not None:
+        _ckpt(me, "z8", z8, M, N, dev)
+    epi = EpilogueC(_vec(me, "bias", bias, N, dev, _FLOATS), rp, ldr,
+                    C.pointer(z8._c) if z8 is not None else None, act,
+                    OUT_BF16 if bias is None else _FLOATS[bias.dtype],
+                    OUT_BF16 if residual is None else _FLOATS[residual.dtype])
+    h = _on_device(me, dev, stream)
+    _check(load().fp4_gemm_epi(C.byref(a.c), C.byref(b.c), alpha, C.byref(epi), cp, ldc,
+                               _FLOATS[out.dtype], _vec(me, "c_amax", c_amax, 1, dev), wsp, wsn, h),
+           me)

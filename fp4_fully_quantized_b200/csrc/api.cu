@@ -379,6 +379,38 @@ fp4_status fp4_gemm_quant_ex(const fp4_qtensor* a, const fp4_qtensor* b, float a
                          c_amax, ws, ws_bytes, stream);
 }
 
+fp4_status fp4_gemm_epi(const fp4_qtensor* a, const fp4_qtensor* b, float alpha,
+                        const fp4_epilogue* epi, void* c, int64_t ldc, int32_t out_dtype,
+                        float* c_amax, void* ws, size_t ws_bytes, void* stream) {
+  if (epi == nullptr) return FP4_ERR_NULL;
+  fp4_status st = gemm_impl(a, b, alpha, c, ldc, out_dtype, c_amax, ws, ws_bytes, stream, true);
+  if (st != FP4_OK) return st;
+  if (!known_act(epi->act)) return FP4_ERR_FORMAT;
+  const int64_t M = a->rows, N = b->rows, K = a->cols;
+  if (epi->bias != nullptr) {
+    if (!known_dtype(epi->bias_dtype)) return FP4_ERR_FORMAT;
+    if (!aligned16(epi->bias)) return FP4_ERR_ALIGN;
+  }
+  if (epi->residual != nullptr) {
+    if (!known_dtype(epi->residual_dtype)) return FP4_ERR_FORMAT;
+    if (epi->ld_residual < N) return FP4_ERR_SHAPE;
+    const int64_t esize = epi->residual_dtype == FP4_OUT_F32 ? 4 : 2;
+    if (!aligned16(epi->residual) || (epi->ld_residual * esize) % 16) return FP4_ERR_ALIGN;
+  }
+  if (epi->z8 != nullptr && (st = check_ckpt8(epi->z8, M, N)) != FP4_OK) return st;
+  GemmArgs g{};
+  g.a_codes = a->codes; g.a_sf = a->scales_mma; g.a_sdec = a->s_dec;
+  g.b_codes = b->codes; g.b_sf = b->scales_mma; g.b_sdec = b->s_dec;
+  g.M = M; g.N = N; g.K = K; g.fmt = a->fmt; g.alpha = alpha;
+  g.c = c; g.ldc = ldc; g.out_mode = out_dtype == FP4_OUT_F32 ? 1 : 0;
+  g.epi = true; g.act = epi->act;
+  g.bias = epi->bias; g.bias_f32 = epi->bias_dtype == FP4_OUT_F32;
+  g.res = epi->residual; g.ldr = epi->ld_residual; g.res_f32 = epi->residual_dtype == FP4_OUT_F32;
+  if (epi->z8 != nullptr) { g.z_codes = epi->z8->codes; g.z_scales = epi->z8->scales; }
+  g.c_amax = c_amax; g.status = status_ptr(ws);
+  return gemm_launch(g, as_stream(stream));
+}
+
 void fqt_linear_cfg_default(fqt_linear_cfg* cfg, int32_t fmt) {
   if (!cfg) return;
   std::memset(cfg, 0, sizeof(*cfg));

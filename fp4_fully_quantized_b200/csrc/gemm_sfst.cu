@@ -29,6 +29,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "act_device.cuh"
 #include "fp4_device.cuh"
 #include "internal.h"
 #include "sm100_ptx.cuh"
@@ -66,6 +67,11 @@ struct StParams {
   int q_sr;                   // out_mode 2: stochastic rounding (else to nearest)
   uint32_t q_stream;          // its Philox stream; keys below
   fp4dev::PhiloxKeys q_keys;
+  // EPI kernels: bias, activation, residual, 8-bit checkpoint
+  int act;
+  const void* bias; bool bias_f32;
+  const void* res; int64_t ldr; bool res_f32;
+  uint8_t* z_codes; uint8_t* z_scales;
   uint32_t* status;
 };
 
@@ -93,7 +99,67 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
 }
 
-template <bool NV>
+// EPI epilogue, one thread: 32 columns from `col` of output row `row`, v = the
+// scaled FP32 products, which become act(v + bias) + residual and are stored.
+// Returns the scale byte of v + bias, a whole block of the checkpoint.
+template <int ACT>
+__device__ __forceinline__ void act32(float* v) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = fp4dev::act_value<ACT>(v[i]);
+}
+
+__device__ __forceinline__ uint32_t epilogue32(const StParams& p, int64_t row, int64_t col, float* v,
+                                               float& amax) {
+  uint32_t byte = 0;
+  if (p.bias != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+      float b[8];
+      fp4dev::load8(p.bias, col + i, p.bias_f32, b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i + j] = __fadd_rn(v[i + j], b[j]);   // no FMA: z is fp4_gemm's P + bias
+    }
+  }
+  if (p.z_codes != nullptr) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m = max(m, fp4dev::abs_bits(v[i]));
+    byte = fp4dev::ckpt_scale_byte(m);
+    const float inv = fp4dev::ckpt_inv_scale(byte);
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[i] = fp4dev::e4m3x4_rn(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+    uint4* d = reinterpret_cast<uint4*>(p.z_codes + row * p.N + col);
+    d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+  switch (p.act) {
+    case FQT_ACT_RELU: act32<FQT_ACT_RELU>(v); break;
+    case FQT_ACT_GELU: act32<FQT_ACT_GELU>(v); break;
+    case FQT_ACT_GELU_TANH: act32<FQT_ACT_GELU_TANH>(v); break;
+    case FQT_ACT_SILU: act32<FQT_ACT_SILU>(v); break;
+    default: break;
+  }
+  if (p.res != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+      float r[8];
+      fp4dev::load8(p.res, row * p.ldr + col + i, p.res_f32, r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i + j] += r[j];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) {
+    fp4dev::store8(p.c, row * p.ldc + col + i, p.out_mode == 1, v + i);
+  }
+  return byte;
+}
+
+template <bool NV, bool EPI>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
                      const __grid_constant__ CUtensorMap tmap_b, const StParams p) {
@@ -304,7 +370,31 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
       const int ncols = min(BN / 2, p.N - nb * BN - c_begin);
       const int64_t col = (int64_t)nb * BN + c_begin;
       const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)c_begin;
-      if (p.out_mode == 0) {
+      if constexpr (EPI) {
+        // four 32-column blocks, one tensor-memory load each
+        uint32_t scales4 = 0;
+#pragma unroll 1
+        for (int h = 0; h < 4; ++h) {
+          uint32_t r[32];
+          tmem_ld32(taddr + 32 * h, r);
+          if (h == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty);
+          }
+          if (ncols > 0) {
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(__uint_as_float(r[i]), scale);
+            scales4 |= epilogue32(p, row, col + 32 * h, v, amax) << (8 * h);
+          }
+        }
+        if (p.z_codes != nullptr && ncols > 0) {
+          *reinterpret_cast<uint32_t*>(p.z_scales + ((row * p.N + col) >> 5)) = scales4;
+          // byte 255: Inf or NaN in one of the four blocks
+          if (__vcmpeq4(scales4, 0xFFFFFFFFu) != 0) set_status(p.status, FP4_ERR_NONFINITE, 8);
+        }
+      } else if (p.out_mode == 0) {
         // drain 128 columns in two 64-column loads, packing to BF16 as they
         // arrive (64 registers); the accumulator is released as soon as the
         // second load has landed, before that half is packed, so the next
@@ -526,23 +616,19 @@ fp4_status gemm_launch(const GemmArgs& g, cudaStream_t s) {
   p.q_codes = g.q_codes; p.q_scales = g.q_scales; p.q_scales_mma = g.q_scales_mma;
   p.q_amax_in = g.q_amax_in; p.q_amax_out = g.q_amax_out; p.q_s_dec = g.q_s_dec;
   p.q_sr = g.q_sr; p.q_stream = g.q_stream; p.q_keys = fp4dev::philox_keys(g.q_seed);
+  p.act = g.act; p.bias = g.bias; p.bias_f32 = g.bias_f32;
+  p.res = g.res; p.ldr = g.ldr; p.res_f32 = g.res_f32;
+  p.z_codes = g.z_codes; p.z_scales = g.z_scales;
   p.c_amax = g.c_amax; p.status = g.status;
   const int tiles = (int)(g.M / BM) * (int)((g.N + BN - 1) / BN);
   const int grid = tiles < sm_count() ? tiles : sm_count();
   if (g.c_amax != nullptr && cudaMemsetAsync(g.c_amax, 0, sizeof(float), s) != cudaSuccess)
     return FP4_ERR_CUDA;
-  cudaError_t e;
-  if (nv) {
-    e = cudaFuncSetAttribute(fp4_gemm_sfst_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             SMEM_BYTES);
-    if (e != cudaSuccess) return FP4_ERR_CUDA;
-    fp4_gemm_sfst_kernel<true><<<grid, NUM_THREADS, SMEM_BYTES, s>>>(ta, tb, p);
-  } else {
-    e = cudaFuncSetAttribute(fp4_gemm_sfst_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             SMEM_BYTES);
-    if (e != cudaSuccess) return FP4_ERR_CUDA;
-    fp4_gemm_sfst_kernel<false><<<grid, NUM_THREADS, SMEM_BYTES, s>>>(ta, tb, p);
-  }
+  const auto kernel = g.epi ? (nv ? fp4_gemm_sfst_kernel<true, true> : fp4_gemm_sfst_kernel<false, true>)
+                            : (nv ? fp4_gemm_sfst_kernel<true, false> : fp4_gemm_sfst_kernel<false, false>);
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess)
+    return FP4_ERR_CUDA;
+  kernel<<<grid, NUM_THREADS, SMEM_BYTES, s>>>(ta, tb, p);
   count_launches(1);
   return cudaGetLastError() == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }

@@ -80,6 +80,37 @@ struct Quant2DArgs {
 };
 cudaError_t launch_quant_2d(const Quant2DArgs& a, cudaStream_t s);
 
+// --- sums over rows (colsum.cu) ----------------------------------------------
+// Kernels that sum over rows (dweight, dbias) write one partial row of sums per
+// row slice behind the status block of the workspace; launch_colsum adds the
+// slices in order, so a result's additions depend on the shape alone.
+constexpr int kMaxSlices = 296;      // two CTAs on each of 148 SMs
+inline int64_t colsum_slices(int64_t rows) { return rows < kMaxSlices ? rows : kMaxSlices; }
+inline float* colsum_partials(void* ws) {
+  return reinterpret_cast<float*>(static_cast<char*>(ws) + sizeof(DeviceStatus));
+}
+cudaError_t launch_colsum(const float* partial, int64_t slices, int64_t cols, float* out,
+                          cudaStream_t s);
+
+// --- argument checks of the calls on [rows, cols] tensors --------------------
+inline bool ptr_aligned(const void* p, uintptr_t n) {
+  return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+// A matrix argument that must be there (rows > 0 checked by the caller).
+inline fp4_status check_matrix(const void* p, int64_t cols, int64_t ld) {
+  if (p == nullptr) return FP4_ERR_NULL;
+  if (ld < cols) return FP4_ERR_SHAPE;
+  return (ptr_aligned(p, 16) && ld % 8 == 0) ? FP4_OK : FP4_ERR_ALIGN;
+}
+inline fp4_status check_ckpt8(const fqt_ckpt8* q, int64_t rows, int64_t cols) {
+  if (q->rows != rows || q->cols != cols || cols % 32 != 0) return FP4_ERR_SHAPE;
+  if (rows == 0) return FP4_OK;
+  if (q->codes == nullptr || q->scales == nullptr) return FP4_ERR_NULL;
+  return ptr_aligned(q->codes, 16) && ptr_aligned(q->scales, 4) ? FP4_OK : FP4_ERR_ALIGN;
+}
+inline bool known_dtype(int32_t t) { return t == FP4_OUT_BF16 || t == FP4_OUT_F32; }
+inline bool known_act(int32_t a) { return a >= FQT_ACT_NONE && a <= FQT_ACT_SILU; }
+
 // --- GEMM (gemm_sfst.cu) ----------------------------------------------------
 struct GemmArgs {
   const uint8_t* a_codes; const uint8_t* a_sf; const float* a_sdec;
@@ -93,6 +124,11 @@ struct GemmArgs {
   uint8_t* q_codes; uint8_t* q_scales; uint8_t* q_scales_mma;
   const float* q_amax_in; float* q_amax_out; float* q_s_dec;
   int q_sr; uint64_t q_seed; uint32_t q_stream;   // out_mode 2 rounding
+  // fp4_gemm_epi (out_mode 0 or 1): C = act(P + bias) + res, checkpoint of P + bias
+  bool epi; int act;
+  const void* bias; bool bias_f32;
+  const void* res; int64_t ldr; bool res_f32;
+  uint8_t* z_codes; uint8_t* z_scales;
   uint32_t* status;
 };
 fp4_status gemm_launch(const GemmArgs& g, cudaStream_t s);

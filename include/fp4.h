@@ -158,7 +158,8 @@ typedef struct fp4_qparams {
 void fp4_qparams_default(fp4_qparams* p);
 
 /* Workspace bytes needed by fp4_gemm for an M x N x K product (also enough
- * for every other entry point).  At least 256: the status block. */
+ * for every other entry point but the sums over rows, see
+ * fqt_colsum_workspace_bytes).  At least 256: the status block. */
 size_t fp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* Quantize x (BF16, [rows, cols] with leading dimension ld >= cols, in
@@ -331,6 +332,123 @@ fp4_status fp4_allreduce_sum_f32(void* nccl_comm, float* buf, int64_t count, voi
 fp4_status fp4_quant_noise(const void* x_bf16, int64_t rows, int64_t cols, int64_t ld,
                            const fp4_qtensor* q, double* sums, void* ws, size_t ws_bytes,
                            void* stream);
+
+/* ---------------------------------------------------------------------- */
+/* What stands between two FP4 linears of a transformer block: activations,  */
+/* RMS norm and residual, with 8-bit checkpoints for the backward pass.      */
+/*                                                                          */
+/* Rules shared by these calls.  Row-major matrices with a leading dimension */
+/* in elements, a multiple of 8 and at least the row length; row lengths     */
+/* are multiples of 8, of 32 where a checkpoint is read or written.  Any     */
+/* number of rows from 0 on.  Sums, statistics and every intermediate are    */
+/* FP32; each output is rounded once.  An output may be the input that its   */
+/* comment names, with the same leading dimension and type; no other buffers */
+/* may overlap.  Results do not depend on the launch configuration, except   */
+/* that column sums over rows are added in an order fixed by the shape       */
+/* alone.  `ws` may be NULL where no workspace size is asked for (device     */
+/* conditions are then not recorded); calls that may run at the same time,   */
+/* replays of captured graphs among them, need workspaces of their own.      */
+/* amax outputs are max |v| of the values as stored in BF16, so that          */
+/* fp4_quantize with that amax_in gives the bits that it gives with its own   */
+/* amax pass; a NaN or Inf among the values shows in the amax.                */
+/* ---------------------------------------------------------------------- */
+enum { FQT_ACT_NONE = 0, FQT_ACT_RELU = 1, FQT_ACT_GELU = 2, FQT_ACT_GELU_TANH = 3,
+       FQT_ACT_SILU = 4 };                        /* GELU: z Phi(z); _TANH its tanh form */
+enum { FQT_RMS_Y = 0, FQT_RMS_XHAT = 1 };         /* what a norm's 8-bit output holds    */
+
+/* An 8-bit checkpoint of a [rows, cols] tensor: codes [rows, cols] E4M3 and
+ * scales [rows, cols/32] E8M0, dense.  A block of 32 consecutive values of a
+ * row shares 2^e (byte e + 127) with the least e >= -127 that gives block
+ * max <= 448 * 2^e; each code is value * 2^-e rounded to nearest even.  A zero
+ * block has byte 0; a block with Inf or NaN has byte 255 and decodes to NaN
+ * (and FP4_ERR_NONFINITE goes to the status word). */
+typedef struct fqt_ckpt8 {
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t rows;
+  int64_t cols;
+} fqt_ckpt8;
+
+/* Bytes of the two buffers (either pointer may be NULL). */
+void fqt_ckpt8_sizes(int64_t rows, int64_t cols, size_t* codes_bytes, size_t* scales_bytes);
+
+/* Workspace bytes of the calls that sum over rows (dweight, dbias) of a
+ * [rows, cols] tensor: the status block and partial sums. */
+size_t fqt_colsum_workspace_bytes(int64_t rows, int64_t cols);
+
+/* RMS norm with the residual's addition:
+ *   s = x + residual (s = x without one),  rstd = (mean_c s^2 + eps)^(-1/2),
+ *   xhat = s * rstd,  y = xhat * weight.
+ * x BF16 [rows, ldx]; residual and res_out (= s) of type res_dtype
+ * (FP4_OUT_BF16 / FP4_OUT_F32), both or neither (res_out may be residual);
+ * weight [cols] of type w_dtype.  Outputs, each NULL when not wanted but y or
+ * q8 needed: y BF16; q8 the 8-bit form of y (q8_of = FQT_RMS_Y) or of xhat
+ * (FQT_RMS_XHAT, the checkpoint fqt_rmsnorm_bwd takes); rstd [rows] float;
+ * y_amax [1] float.  The statistics and y come from the unrounded s.
+ * cols <= 32768; eps > 0; s^2 must not overflow FP32. */
+fp4_status fqt_rmsnorm_fwd(const void* x_bf16, int64_t ldx, const void* residual, int64_t ldr,
+                           void* res_out, int64_t ldo, int32_t res_dtype, const void* weight,
+                           int32_t w_dtype, float eps, int64_t rows, int64_t cols, void* y_bf16,
+                           int64_t ldy, const fqt_ckpt8* q8, int32_t q8_of, float* rstd,
+                           float* y_amax, void* ws, size_t ws_bytes, void* stream);
+
+/* Its backward: with g = dy * weight,
+ *   dx = rstd * (g - xhat * mean_c(g * xhat)) + dres,
+ *   dweight[c] = sum over rows of dy * xhat,
+ * the gradient of both x and the residual, and the weight's (FP32,
+ * overwritten; NULL when not wanted).  xhat comes from the checkpoint `xhat8`
+ * or as s * rstd from the stored sum `s` (type s_dtype): exactly one of the
+ * two.  dy BF16; dres (nullable, the gradient arriving along the residual
+ * stream) and dx of type grad_dtype, dx may be dres.  With dweight, ws must
+ * hold fqt_colsum_workspace_bytes(rows, cols). */
+fp4_status fqt_rmsnorm_bwd(const void* dy_bf16, int64_t lddy, const void* s, int64_t lds,
+                           int32_t s_dtype, const fqt_ckpt8* xhat8, const float* rstd,
+                           const void* weight, int32_t w_dtype, const void* dres, int64_t lddres,
+                           void* dx, int64_t lddx, int32_t grad_dtype, int64_t rows, int64_t cols,
+                           float* dweight, void* ws, size_t ws_bytes, void* stream);
+
+/* Activation forward.  gated == 0: y = act(z), z [rows, cols]; gated != 0:
+ * y = act(z[:, :cols]) * z[:, cols:], z [rows, 2 cols].  z comes as BF16 (`z`,
+ * leading dimension ldz) or from a checkpoint (`z8_in`: the recomputation of
+ * y; with FQT_ACT_NONE the checkpoint's decoding): exactly one of the two.
+ * Outputs: y BF16 [rows, cols]; z8_out the checkpoint of a BF16 z (with y
+ * NULL: encoding alone); y_amax.  y or z8_out is needed, y_amax needs y. */
+fp4_status fqt_act_fwd(const void* z_bf16, int64_t ldz, const fqt_ckpt8* z8_in, int32_t act,
+                       int32_t gated, int64_t rows, int64_t cols, void* y_bf16, int64_t ldy,
+                       const fqt_ckpt8* z8_out, float* y_amax, void* ws, size_t ws_bytes,
+                       void* stream);
+
+/* Its backward: dz = dy * act'(z), or [dy * z[:, cols:] * act'(z[:, :cols]),
+ * dy * act(z[:, :cols])] when gated; z as above.  dy BF16 [rows, cols]; dz
+ * BF16 of z's shape (may be z, or dy when not gated); dbias (nullable) FP32
+ * [z's row length], overwritten with the sums of the unrounded dz over the
+ * rows; dz_amax nullable.  act' of ReLU at 0 is 0.  With dbias, ws must hold
+ * fqt_colsum_workspace_bytes(rows, z's row length). */
+fp4_status fqt_act_bwd(const void* dy_bf16, int64_t lddy, const void* z_bf16, int64_t ldz,
+                       const fqt_ckpt8* z8, int32_t act, int32_t gated, int64_t rows, int64_t cols,
+                       void* dz_bf16, int64_t lddz, float* dbias, float* dz_amax, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/* fp4_gemm with an epilogue on its FP32 result P (as fp4_gemm computes it):
+ *   z = P + bias[n],  C = act(z) + residual,
+ * one rounding at the store.  bias [N] and residual [M, ld_residual] (its row
+ * start a multiple of 16 bytes; it may be c itself when type and leading
+ * dimension agree) may each be NULL and are of the given types; z8 (nullable)
+ * receives the checkpoint of z, [M, N], which fqt_act_bwd takes.  c_amax
+ * receives max |C| of the FP32 values.  All else as fp4_gemm. */
+typedef struct fp4_epilogue {
+  const void* bias;
+  const void* residual;
+  int64_t ld_residual;
+  const fqt_ckpt8* z8;
+  int32_t act;              /* FQT_ACT_*                    */
+  int32_t bias_dtype;       /* FP4_OUT_BF16 / FP4_OUT_F32   */
+  int32_t residual_dtype;   /* FP4_OUT_BF16 / FP4_OUT_F32   */
+} fp4_epilogue;
+
+fp4_status fp4_gemm_epi(const fp4_qtensor* a, const fp4_qtensor* b, float alpha,
+                        const fp4_epilogue* epi, void* c, int64_t ldc, int32_t out_dtype,
+                        float* c_amax, void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, then return the device status word of `ws`
  * (FP4_OK when no device condition was recorded). */
