@@ -478,7 +478,12 @@ class Ckpt8:
                      Ckpt8C(codes.data_ptr(), scales.data_ptr(), rows, cols))
 
 
-_FLOATS = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
+_BF16, _F32 = torch.bfloat16, torch.float32
+_FLOATS = {_BF16: OUT_BF16, _F32: OUT_F32}
+# the current stream's handle without making a Stream object (a microsecond of
+# the ten that a small call takes)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _bad(where, name, t, want):
@@ -486,53 +491,55 @@ def _bad(where, name, t, want):
     raise ValueError(f"{where}: {name} must be {want}, got {got}")
 
 
-def _mat(where, name, t, rows, cols, device, types=(torch.bfloat16,)):
-    """Pointer and leading dimension of a [rows, cols] matrix, (None, 0) for None."""
-    if t is None:
-        return None, 0
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or t.dtype not in types or \
-            t.device != device or (t.stride(1) != 1 and cols > 1):
-        _bad(where, name, t, f"a [{rows}, {cols}] row-major matrix of {types} on {device}")
-    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+def _ld(where, name, t, shape, dev, f32=False):
+    """Leading dimension of a row-major matrix of `shape` on device `dev`, BF16
+    (or FP32 where f32)."""
+    strides = t.stride()
+    if t.shape != shape or t.get_device() != dev or strides[1] != 1 or \
+            (t.dtype is not _BF16 and not (f32 and t.dtype is _F32)):
+        _bad(where, name, t, f"a {list(shape)} row-major matrix of BF16{' or FP32' if f32 else ''} "
+                             f"on device {dev}")
+    return strides[0] if shape[0] > 1 else shape[1]
 
 
-def _vec(where, name, t, n, device, types=(torch.float32,)):
+def _vec(where, name, t, n, dev, bf16=False):
+    """Pointer of a dense FP32 (or BF16 where bf16) vector of n, None for None."""
     if t is None:
         return None
-    if t.dim() != 1 or t.shape[0] != n or t.dtype not in types or t.device != device or \
-            not t.is_contiguous():
-        _bad(where, name, t, f"a dense vector of {n} {types} on {device}")
+    if t.shape != (n,) or t.get_device() != dev or (n > 1 and t.stride(0) != 1) or \
+            (t.dtype is not _F32 and not (bf16 and t.dtype is _BF16)):
+        _bad(where, name, t, f"a dense vector of {n} FP32{' or BF16' if bf16 else ''} on device {dev}")
     return t.data_ptr()
 
 
-def _ckpt(where, name, q, rows, cols, device):
+def _ckpt(where, name, q, rows, cols, dev):
     if q is None:
         return None
-    if not isinstance(q, Ckpt8) or q.rows != rows or q.cols != cols or q.codes.device != device:
-        _bad(where, name, q, f"a Ckpt8 of [{rows}, {cols}] on {device}")
+    if not isinstance(q, Ckpt8) or q.rows != rows or q.cols != cols or q.codes.get_device() != dev:
+        _bad(where, name, q, f"a Ckpt8 of [{rows}, {cols}] on device {dev}")
     return C.byref(q._c)
 
 
-def _work(where, ws, device):
+def _work(where, ws, dev):
     if ws is None:
         return None, 0
-    if ws.buf.device != device:
-        _bad(where, "ws", ws.buf, f"a workspace on {device}")
+    if ws.buf.get_device() != dev:
+        _bad(where, "ws", ws.buf, f"a workspace on device {dev}")
     return ws.buf.data_ptr(), ws.buf.numel()
 
 
-def _on_device(where, device, stream):
-    """The stream's handle, with `device` checked to be the current device:
-    kernels launch on the current one."""
-    if device.type != "cuda":
-        raise ValueError(f"{where}: tensors must be on a CUDA device, got {device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"{where}: tensors are on {device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()} (use torch.cuda.device)")
+def _on_device(where, dev, stream):
+    """The stream's handle, with `dev` checked to be the current device: kernels
+    launch on the current one."""
+    if dev < 0:
+        raise ValueError(f"{where}: tensors must be on a CUDA device")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{where}: tensors are on device {dev}, the current device is "
+                         f"{torch.cuda.current_device()} (use torch.cuda.device)")
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    if stream.device != device:
-        raise ValueError(f"{where}: stream of {stream.device}, tensors on {device}")
+        return _raw_stream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"{where}: stream of {stream.device}, tensors on device {dev}")
     return stream.cuda_stream
 
 
@@ -545,24 +552,29 @@ def fqt_rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor | Non
     q8 receives the 8-bit form of y (RMS_Y) or of s * rstd (RMS_XHAT, what
     fqt_rmsnorm_bwd takes).  x, y BF16; residual and res_out both BF16 or both
     FP32 (res_out may be residual); weight BF16 or FP32."""
-    me, dev = "fqt_rmsnorm_fwd", x.device
-    if x.dim() != 2:
+    me, dev, shape = "fqt_rmsnorm_fwd", x.get_device(), x.shape
+    if len(shape) != 2:
         _bad(me, "x", x, "a matrix")
-    rows, cols = x.shape
-    xp, ldx = _mat(me, "x", x, rows, cols, dev)
-    rp, ldr = _mat(me, "residual", residual, rows, cols, dev, _FLOATS)
-    op, ldo = _mat(me, "res_out", res_out, rows, cols, dev, _FLOATS)
-    if (residual is None) != (res_out is None) or (residual is not None and
-                                                   residual.dtype != res_out.dtype):
+    rows, cols = shape
+    ldx = _ld(me, "x", x, shape, dev)
+    rp, ldr, op, ldo, rt, yp, ldy = None, 0, None, 0, OUT_BF16, None, 0
+    if residual is not None and res_out is not None and residual.dtype is res_out.dtype:
+        rp, ldr = residual.data_ptr(), _ld(me, "residual", residual, shape, dev, True)
+        op, ldo = res_out.data_ptr(), _ld(me, "res_out", res_out, shape, dev, True)
+        rt = _FLOATS[residual.dtype]
+    elif residual is not None or res_out is not None:
         raise ValueError(f"{me}: residual and res_out go together and have one type")
-    yp, ldy = _mat(me, "y", y, rows, cols, dev)
-    wp = _vec(me, "weight", weight, cols, dev, _FLOATS)
+    if y is not None:
+        yp, ldy = y.data_ptr(), _ld(me, "y", y, shape, dev)
+    wp = _vec(me, "weight", weight, cols, dev, True)
     wsp, wsn = _work(me, ws, dev)
     h = _on_device(me, dev, stream)
-    _check(load().fqt_rmsnorm_fwd(
-        xp, ldx, rp, ldr, op, ldo, OUT_BF16 if residual is None else _FLOATS[residual.dtype], wp,
-        _FLOATS[weight.dtype], eps, rows, cols, yp, ldy, _ckpt(me, "q8", q8, rows, cols, dev), q8_of,
-        _vec(me, "rstd", rstd, rows, dev), _vec(me, "y_amax", y_amax, 1, dev), wsp, wsn, h), me)
+    code = (_lib or load()).fqt_rmsnorm_fwd(
+        x.data_ptr(), ldx, rp, ldr, op, ldo, rt, wp, _FLOATS[weight.dtype], eps, rows, cols, yp, ldy,
+        _ckpt(me, "q8", q8, rows, cols, dev), q8_of, _vec(me, "rstd", rstd, rows, dev),
+        _vec(me, "y_amax", y_amax, 1, dev), wsp, wsn, h)
+    if code:
+        raise Fp4Error(code, me)
 
 
 def fqt_rmsnorm_bwd(dy: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, dx: torch.Tensor,
@@ -574,36 +586,33 @@ def fqt_rmsnorm_bwd(dy: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, 
     checkpoint `xhat8` or as s * rstd.  dres and dx have one type, BF16 or
     FP32 (dx may be dres).  With dweight, ws is Workspace.colsum(rows, cols)
     (made here when None)."""
-    me, dev = "fqt_rmsnorm_bwd", dy.device
-    if dy.dim() != 2:
+    me, dev, shape = "fqt_rmsnorm_bwd", dy.get_device(), dy.shape
+    if len(shape) != 2:
         _bad(me, "dy", dy, "a matrix")
-    rows, cols = dy.shape
+    rows, cols = shape
     if (s is None) == (xhat8 is None):
         raise ValueError(f"{me}: exactly one of s and xhat8")
-    dyp, lddy = _mat(me, "dy", dy, rows, cols, dev)
-    sp, lds = _mat(me, "s", s, rows, cols, dev, _FLOATS)
-    drp, lddr = _mat(me, "dres", dres, rows, cols, dev, _FLOATS)
-    dxp, lddx = _mat(me, "dx", dx, rows, cols, dev, _FLOATS)
-    if dres is not None and dres.dtype != dx.dtype:
-        raise ValueError(f"{me}: dres and dx have one type")
-    wp = _vec(me, "weight", weight, cols, dev, _FLOATS)
-    if dweight is not None and ws is None:
-        ws = Workspace.colsum(rows, cols, device=dev)
-    wsp, wsn = _work(me, ws, dev)
+    lddy = _ld(me, "dy", dy, shape, dev)
+    sp, lds, st, drp, lddr = None, 0, OUT_BF16, None, 0
+    if s is not None:
+        sp, lds, st = s.data_ptr(), _ld(me, "s", s, shape, dev, True), _FLOATS[s.dtype]
+    lddx = _ld(me, "dx", dx, shape, dev, True)
+    if dres is not None:
+        if dres.dtype is not dx.dtype:
+            raise ValueError(f"{me}: dres and dx have one type")
+        drp, lddr = dres.data_ptr(), _ld(me, "dres", dres, shape, dev, True)
+    wp = _vec(me, "weight", weight, cols, dev, True)
+    dwp = _vec(me, "dweight", dweight, cols, dev)
     h = _on_device(me, dev, stream)
-    _check(load().fqt_rmsnorm_bwd(
-        dyp, lddy, sp, lds, OUT_BF16 if s is None else _FLOATS[s.dtype],
-        _ckpt(me, "xhat8", xhat8, rows, cols, dev), _vec(me, "rstd", rstd, rows, dev), wp,
-        _FLOATS[weight.dtype], drp, lddr, dxp, lddx, _FLOATS[dx.dtype], rows, cols,
-        _vec(me, "dweight", dweight, cols, dev), wsp, wsn, h), me)
-
-
-def _z(me, z, rows, zcols, dev):
-    """(pointer, leading dimension, checkpoint) of a z given as a matrix or a Ckpt8."""
-    if isinstance(z, Ckpt8):
-        return None, 0, _ckpt(me, "z", z, rows, zcols, dev)
-    zp, ldz = _mat(me, "z", z, rows, zcols, dev)
-    return zp, ldz, None
+    if dwp is not None and ws is None:
+        ws = Workspace.colsum(rows, cols, device=dy.device)
+    wsp, wsn = _work(me, ws, dev)
+    code = (_lib or load()).fqt_rmsnorm_bwd(
+        dy.data_ptr(), lddy, sp, lds, st, _ckpt(me, "xhat8", xhat8, rows, cols, dev),
+        _vec(me, "rstd", rstd, rows, dev), wp, _FLOATS[weight.dtype], drp, lddr, dx.data_ptr(), lddx,
+        _FLOATS[dx.dtype], rows, cols, dwp, wsp, wsn, h)
+    if code:
+        raise Fp4Error(code, me)
 
 
 def fqt_act_fwd(z, y: torch.Tensor | None = None, act: int = ACT_SILU, gated: bool = False,
@@ -612,20 +621,27 @@ def fqt_act_fwd(z, y: torch.Tensor | None = None, act: int = ACT_SILU, gated: bo
     """y = act(z), or act(z[:, :F]) * z[:, F:] with gated (z [rows, 2 F]).  z is a
     BF16 matrix, or a Ckpt8 (recomputation; with ACT_NONE its decoding).  z8
     receives the 8-bit checkpoint of a matrix z (y None: encoding alone)."""
-    me = "fqt_act_fwd"
+    me, zp, ldz, zc = "fqt_act_fwd", None, 0, None
     src = z.codes if isinstance(z, Ckpt8) else z
-    dev = src.device
-    if src.dim() != 2 or (gated and src.shape[1] % 2):
+    dev, zshape = src.get_device(), src.shape
+    if len(zshape) != 2 or (gated and zshape[1] % 2):
         _bad(me, "z", src, "a matrix, with an even row length when gated")
-    rows, zcols = src.shape
+    rows, zcols = zshape
     cols = zcols // 2 if gated else zcols
-    zp, ldz, zc = _z(me, z, rows, zcols, dev)
-    yp, ldy = _mat(me, "y", y, rows, cols, dev)
+    if src is z:
+        zp, ldz = z.data_ptr(), _ld(me, "z", z, zshape, dev)
+    else:
+        zc = _ckpt(me, "z", z, rows, zcols, dev)
+    yp, ldy = None, 0
+    if y is not None:
+        yp, ldy = y.data_ptr(), _ld(me, "y", y, (rows, cols), dev)
     wsp, wsn = _work(me, ws, dev)
     h = _on_device(me, dev, stream)
-    _check(load().fqt_act_fwd(zp, ldz, zc, act, 1 if gated else 0, rows, cols, yp, ldy,
-                              _ckpt(me, "z8", z8, rows, zcols, dev),
-                              _vec(me, "y_amax", y_amax, 1, dev), wsp, wsn, h), me)
+    code = (_lib or load()).fqt_act_fwd(
+        zp, ldz, zc, act, 1 if gated else 0, rows, cols, yp, ldy,
+        _ckpt(me, "z8", z8, rows, zcols, dev), _vec(me, "y_amax", y_amax, 1, dev), wsp, wsn, h)
+    if code:
+        raise Fp4Error(code, me)
 
 
 def fqt_act_bwd(dy: torch.Tensor, z, dz: torch.Tensor, act: int = ACT_SILU, gated: bool = False,
@@ -635,21 +651,27 @@ def fqt_act_bwd(dy: torch.Tensor, z, dz: torch.Tensor, act: int = ACT_SILU, gate
     [dy * z[:, F:] * act'(z[:, :F]), dy * act(z[:, :F])].  dbias (FP32): sums of dz
     over the rows; ws is then Workspace.colsum(rows, z's row length) (made here
     when None)."""
-    me, dev = "fqt_act_bwd", dy.device
-    if dy.dim() != 2:
+    me, dev, shape = "fqt_act_bwd", dy.get_device(), dy.shape
+    if len(shape) != 2:
         _bad(me, "dy", dy, "a matrix")
-    rows, cols = dy.shape
+    rows, cols = shape
     zcols = 2 * cols if gated else cols
-    dyp, lddy = _mat(me, "dy", dy, rows, cols, dev)
-    zp, ldz, zc = _z(me, z, rows, zcols, dev)
-    dzp, lddz = _mat(me, "dz", dz, rows, zcols, dev)
-    if dbias is not None and ws is None:
-        ws = Workspace.colsum(rows, zcols, device=dev)
-    wsp, wsn = _work(me, ws, dev)
+    lddy, zp, ldz, zc = _ld(me, "dy", dy, shape, dev), None, 0, None
+    if isinstance(z, Ckpt8):
+        zc = _ckpt(me, "z", z, rows, zcols, dev)
+    else:
+        zp, ldz = z.data_ptr(), _ld(me, "z", z, (rows, zcols), dev)
+    lddz = _ld(me, "dz", dz, (rows, zcols), dev)
+    dbp = _vec(me, "dbias", dbias, zcols, dev)
     h = _on_device(me, dev, stream)
-    _check(load().fqt_act_bwd(dyp, lddy, zp, ldz, zc, act, 1 if gated else 0, rows, cols, dzp, lddz,
-                              _vec(me, "dbias", dbias, zcols, dev),
-                              _vec(me, "dz_amax", dz_amax, 1, dev), wsp, wsn, h), me)
+    if dbp is not None and ws is None:
+        ws = Workspace.colsum(rows, zcols, device=dy.device)
+    wsp, wsn = _work(me, ws, dev)
+    code = (_lib or load()).fqt_act_bwd(
+        dy.data_ptr(), lddy, zp, ldz, zc, act, 1 if gated else 0, rows, cols, dz.data_ptr(), lddz, dbp,
+        _vec(me, "dz_amax", dz_amax, 1, dev), wsp, wsn, h)
+    if code:
+        raise Fp4Error(code, me)
 
 
 def fp4_gemm_epi(a: QTensor, b: QTensor, out: torch.Tensor, alpha: float = 1.0,
@@ -659,23 +681,27 @@ def fp4_gemm_epi(a: QTensor, b: QTensor, out: torch.Tensor, alpha: float = 1.0,
     """out = act(z) + residual with z = (fp4_gemm's FP32 result) + bias; z8 receives
     the 8-bit checkpoint of z.  bias [N] and residual [M, N] BF16 or FP32
     (residual may be out itself)."""
-    me, dev = "fp4_gemm_epi", out.device
-    M, N = a.rows, b.rows
-    for name, q in (("a", a), ("b", b)):
-        if q.codes.device != dev:
-            _bad(me, name, q.codes, f"an operand on {dev}")
-    cp, ldc = _mat(me, "out", out, M, N, dev, _FLOATS)
-    rp, ldr = _mat(me, "residual", residual, M, N, dev, _FLOATS)
-    if ws is None:
-        ws = Workspace(M, N, a.cols, device=dev)
-    wsp, wsn = _work(me, ws, dev)
+    me, dev, M, N = "fp4_gemm_epi", out.get_device(), a.rows, b.rows
+    if a.codes.get_device() != dev or b.codes.get_device() != dev:
+        _bad(me, "a and b", a.codes, f"operands on device {dev}")
+    ldc = _ld(me, "out", out, (M, N), dev, True)
+    rp, ldr, rt, bt = None, 0, OUT_BF16, OUT_BF16
+    if residual is not None:
+        rp, ldr = residual.data_ptr(), _ld(me, "residual", residual, (M, N), dev, True)
+        rt = _FLOATS[residual.dtype]
+    bp = _vec(me, "bias", bias, N, dev, True)
+    if bp is not None:
+        bt = _FLOATS[bias.dtype]
+    zc = None
     if z8 is not None:
         _ckpt(me, "z8", z8, M, N, dev)
-    epi = EpilogueC(_vec(me, "bias", bias, N, dev, _FLOATS), rp, ldr,
-                    C.pointer(z8._c) if z8 is not None else None, act,
-                    OUT_BF16 if bias is None else _FLOATS[bias.dtype],
-                    OUT_BF16 if residual is None else _FLOATS[residual.dtype])
+        zc = C.pointer(z8._c)
     h = _on_device(me, dev, stream)
-    _check(load().fp4_gemm_epi(C.byref(a.c), C.byref(b.c), alpha, C.byref(epi), cp, ldc,
-                               _FLOATS[out.dtype], _vec(me, "c_amax", c_amax, 1, dev), wsp, wsn, h),
-           me)
+    if ws is None:
+        ws = Workspace(M, N, a.cols, device=out.device)
+    wsp, wsn = _work(me, ws, dev)
+    code = (_lib or load()).fp4_gemm_epi(
+        C.byref(a.c), C.byref(b.c), alpha, C.byref(EpilogueC(bp, rp, ldr, zc, act, bt, rt)),
+        out.data_ptr(), ldc, _FLOATS[out.dtype], _vec(me, "c_amax", c_amax, 1, dev), wsp, wsn, h)
+    if code:
+        raise Fp4Error(code, me)

@@ -230,7 +230,7 @@ fp4_status fqt_act_fwd(const void* z, int64_t ldz, const fqt_ckpt8* z8_in, int32
   const int64_t zcols = gated ? 2 * cols : cols;
   fp4_status st = check_act(z, ldz, z8_in, act, rows, cols, zcols, ws, ws_bytes);
   if (st != FP4_OK) return st;
-  if ((y == nullptr && z8_out == nullptr) || (y == nullptr && y_amax != nullptr)) return FP4_ERR_NULL;
+  if (rows > 0 && y == nullptr && (z8_out == nullptr || y_amax != nullptr)) return FP4_ERR_NULL;
   if (z8_in != nullptr && z8_out != nullptr) return FP4_ERR_FORMAT;
   if (y != nullptr && rows > 0 && (st = check_matrix(y, cols, ldy)) != FP4_OK) return st;
   if (z8_out != nullptr) {

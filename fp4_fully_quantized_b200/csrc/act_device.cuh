@@ -59,6 +59,13 @@ __device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float* v) {
   v[0] = f0.x; v[1] = f0.y; v[2] = f1.x; v[3] = f1.y;
 }
 
+// max(m, |a|, |b|) for m >= 0, NaN if one of them is.
+__device__ __forceinline__ float max_abs3(float m, float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
 // ---------------------------------------------------------------------------
@@ -71,13 +78,34 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 
+// The normal CDF and e = exp(-z^2/2), by the rational approximation of erfc of
+// Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26: for x >= 0
+// erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), to
+// 1.5e-7, with x = |z| / sqrt(2) (so the exponential is the density's too, and
+// the lower tail is not a difference).  An absolute error of 0.75e-7 is one
+// and a quarter units of FP32's last place at 1.
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  const float t = __fdividef(1.0f, 1.0f + 0.23164190f * fabsf(z));   // 0.3275911 / sqrt(2)
+  e = __expf(-0.5f * z * z);
+  float q = 1.061405429f;
+  q = q * t - 1.453152027f;
+  q = q * t + 1.421413741f;
+  q = q * t - 0.284496736f;
+  q = q * t + 0.254829592f;
+  const float tail = 0.5f * (q * t) * e;
+  return z < 0.0f ? tail : 1.0f - tail;
+}
+
 constexpr float kTwoC = 1.5957691216057308f;          // 2 sqrt(2/pi)
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == FQT_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
   if constexpr (ACT == FQT_ACT_SILU) return z * logistic(z);
-  if constexpr (ACT == FQT_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  if constexpr (ACT == FQT_ACT_GELU) {
+    float e;
+    return z * normal_cdf(z, e);
+  }
   if constexpr (ACT == FQT_ACT_GELU_TANH)
     return z * logistic(kTwoC * z * (1.0f + 0.044715f * fminf(z * z, 1e4f)));
   return z;
@@ -97,9 +125,10 @@ __device__ __forceinline__ void act_both(float z, float& f, float& df) {
     df = p + f * (1.0f - p);
   }
   if constexpr (ACT == FQT_ACT_GELU) {
-    const float cdf = 0.5f + 0.5f * erff(z * 0.70710678118654752f);
+    float e;
+    const float cdf = normal_cdf(z, e);
     f = z * cdf;
-    df = cdf + z * (0.3989422804014327f * __expf(-0.5f * z * z));
+    df = cdf + z * (0.3989422804014327f * e);
   }
   if constexpr (ACT == FQT_ACT_GELU_TANH) {
     const float z2 = fminf(z * z, 1e4f);

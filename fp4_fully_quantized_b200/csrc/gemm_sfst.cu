@@ -71,7 +71,7 @@ struct StParams {
   int act;
   const void* bias; bool bias_f32;
   const void* res; int64_t ldr; bool res_f32;
-  uint8_t* z_codes; uint8_t* z_scales;
+  uint8_t* z_codes; uint8_t* z_scales; bool z_wide;   // codes 32-byte aligned
   uint32_t* status;
 };
 
@@ -109,7 +109,7 @@ __device__ __forceinline__ void act32(float* v) {
 }
 
 __device__ __forceinline__ uint32_t epilogue32(const StParams& p, int64_t row, int64_t col, float* v,
-                                               float& amax) {
+                                               bool wide_st, float& amax) {
   uint32_t byte = 0;
   if (p.bias != nullptr) {
 #pragma unroll
@@ -121,18 +121,23 @@ __device__ __forceinline__ uint32_t epilogue32(const StParams& p, int64_t row, i
     }
   }
   if (p.z_codes != nullptr) {
-    uint32_t m = 0;
+    float m = fabsf(v[31]);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) m = max(m, fp4dev::abs_bits(v[i]));
-    byte = fp4dev::ckpt_scale_byte(m);
+    for (int i = 0; i < 30; i += 2) m = fp4dev::max_abs3(m, v[i], v[i + 1]);
+    m = fp4dev::max_abs3(m, v[30], v[30]);
+    byte = fp4dev::ckpt_scale_byte(fp4dev::abs_bits(m));
     const float inv = fp4dev::ckpt_inv_scale(byte);
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       w[i] = fp4dev::e4m3x4_rn(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
-    uint4* d = reinterpret_cast<uint4*>(p.z_codes + row * p.N + col);
-    d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    uint8_t* d = p.z_codes + row * p.N + col;                             // a multiple of 32 from the start
+    if (p.z_wide) {
+      st_global_v8(d, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+    } else {
+      reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
   }
   switch (p.act) {
     case FQT_ACT_RELU: act32<FQT_ACT_RELU>(v); break;
@@ -150,13 +155,46 @@ __device__ __forceinline__ uint32_t epilogue32(const StParams& p, int64_t row, i
       for (int j = 0; j < 8; ++j) v[i + j] += r[j];
     }
   }
+  if (p.c_amax != nullptr) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));
+    for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));
+  }
+  if (p.out_mode == 1) {
+    float* d = static_cast<float*>(p.c) + row * p.ldc + col;
 #pragma unroll
-  for (int i = 0; i < 32; i += 8) {
-    fp4dev::store8(p.c, row * p.ldc + col + i, p.out_mode == 1, v + i);
+    for (int i = 0; i < 32; i += 8) {
+      if (wide_st)
+        st_global_v8(d + i, __float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]),
+                     __float_as_uint(v[i + 3]), __float_as_uint(v[i + 4]), __float_as_uint(v[i + 5]),
+                     __float_as_uint(v[i + 6]), __float_as_uint(v[i + 7]));
+      else
+        fp4dev::store8(d, i, true, v + i);
+    }
+  } else {
+    __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.c) + row * p.ldc + col;
+#pragma unroll
+    for (int i = 0; i < 32; i += 16) {
+      const uint4 lo = fp4dev::pack_bf16x8(v + i), hi = fp4dev::pack_bf16x8(v + i + 8);
+      if (wide_st) {
+        st_global_v8(d + i, lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w);
+      } else {
+        reinterpret_cast<uint4*>(d + i)[0] = lo;
+        reinterpret_cast<uint4*>(d + i)[1] = hi;
+      }
+    }
   }
   return byte;
+}
+
+// Registers of an EPI kernel's warpgroups (four warps each): the epilogue's two
+// hold a row's 128 accumulator columns at once, so that the accumulator is free
+// for the next tile's MMAs before any of the epilogue's arithmetic.  The sum is
+// what the 512 threads are launched with, 4 x 128.
+constexpr int kEpiRegs = 184, kOtherRegs = 72;
+static_assert(2 * kEpiRegs + 2 * kOtherRegs <= 4 * 128, "register split");
+template <bool EPI>
+__device__ __forceinline__ void fewer_registers() {
+  if constexpr (EPI) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
 }
 
 template <bool NV, bool EPI>
@@ -209,50 +247,9 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-
-  if (warp == PRODUCER_WARP) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_b)) : "memory");
-      uint32_t it = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x) {
-        int mb, nb;
-        tile_coords(tile, tiles_m, tiles_n, mb, nb);
-        const bool b_hi = (nb * 2 + 1) * 128 < p.N;
-        for (int kb = 0; kb < k_blocks; ++kb, ++it) {
-          const int s = it % STAGES;
-          const uint32_t ph = (it / STAGES) & 1u;
-          if (!mbar_wait(empty_bar(s), ph ^ 1u, abort_flag, p.status, 0x3100 + s)) { ok = false; break; }
-          const int n_atoms = NV ? min(4, apr - kb * 4) : min(2, apr - kb * 2);
-          const uint32_t atom_bytes = (uint32_t)n_atoms * 512u;
-          // scale atoms first, on their own barrier: the stagers move them into
-          // tensor memory while the operand tiles are still in flight
-          mbar_arrive_expect_tx(atoms_bar(s), atom_bytes * (b_hi ? 3u : 2u));
-          const int atom0 = kb * (NV ? 4 : 2);
-          bulk_load(smem_u32(sSFA(s)), p.a_sf + ((size_t)mb * apr + atom0) * 512, atom_bytes,
-                    atoms_bar(s));
-          bulk_load(smem_u32(sSFB(s)), p.b_sf + ((size_t)(2 * nb) * apr + atom0) * 512, atom_bytes,
-                    atoms_bar(s));
-          if (b_hi)
-            bulk_load(smem_u32(sSFB(s) + 4 * 512), p.b_sf + ((size_t)(2 * nb + 1) * apr + atom0) * 512,
-                      atom_bytes, atoms_bar(s));
-          mbar_arrive_expect_tx(full_bar(s), A_BYTES + B_BYTES);
-          tma_load_2d(smem_u32(sA(s)), &tmap_a, full_bar(s), kb * (BK / 2), mb * BM);
-          tma_load_2d(smem_u32(sB(s)), &tmap_b, full_bar(s), kb * (BK / 2), nb * BN);
-        }
-      }
-      if (it > 0) {
-        const uint32_t first = it > (uint32_t)STAGES ? it - STAGES : 0;
-        for (uint32_t j = first; j < it; ++j) {
-          volatile int no_abort = 0;
-          mbar_wait(atoms_bar(j % STAGES), (j / STAGES) & 1u, &no_abort, p.status, 0x3200 + j % STAGES);
-          mbar_wait(full_bar(j % STAGES), (j / STAGES) & 1u, &no_abort, p.status, 0x3200 + j % STAGES);
-        }
-      }
-    }
-  } else if (warp < SF_WARP0 + 4) {
+  // one branch per warpgroup: a register split is the whole warpgroup's
+  if (warp < SF_WARP0 + 4) {
+    fewer_registers<EPI>();
     // ------------------------------------------------------------ scale stagers
     // Tensor-memory scale layout the MMA reads (what a 32x128b.warpx4 copy of
     // a 512-byte atom produces): every lane quadrant holds the whole atom,
@@ -287,59 +284,8 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
         if (lane == 0) mbar_arrive(sf_bar(s));
       }
     }
-  } else if (warp == MMA_WARP) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      uint32_t it = 0, tile_iter = 0;
-      bool ok = true, issued = false;
-      for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x, ++tile_iter) {
-        if (!mbar_wait(acc_empty, (tile_iter & 1u) ^ 1u, abort_flag, p.status, 0x3400)) { ok = false; break; }
-        tc_fence_after();
-        for (int kb = 0; kb < k_blocks; ++kb, ++it) {
-          const int s = it % STAGES;
-          const uint32_t ph = (it / STAGES) & 1u;
-          if (!mbar_wait(sf_bar(s), ph, abort_flag, p.status, 0x3500 + s)) { ok = false; break; }
-          if (!mbar_wait(full_bar(s), ph, abort_flag, p.status, 0x3580 + s)) { ok = false; break; }
-          tc_fence_after();
-          const int n_mma = min(BK / MMA_K, (p.K - kb * BK) / MMA_K);
-          const uint32_t t_sfa = tmem_base + TMEM_SF_BASE + s * TMEM_SF_STAGE;
-          const uint32_t t_sfb = t_sfa + 16;
-          const uint32_t a_base = smem_u32(sA(s)), b_base = smem_u32(sB(s));
-          auto step = [&](int kk) {
-            uint32_t sfa_addr, sfb_addr, idesc;
-            if (NV) {
-              sfa_addr = t_sfa + 4 * kk;
-              sfb_addr = t_sfb + 8 * kk;
-              idesc = make_idesc(BN, BM, 0u, 0u, 0u);
-            } else {
-              const uint32_t byte = (uint32_t)(kk & 1) * 2u;
-              sfa_addr = (t_sfa + 4 * (kk >> 1)) | (byte << 30);
-              sfb_addr = (t_sfb + 8 * (kk >> 1)) | (byte << 30);
-              idesc = make_idesc(BN, BM, 1u, byte, byte);
-            }
-            tc_mma<NV>(tmem_base, smem_desc(a_base + kk * (MMA_K / 2), 16, 1024, 2),
-                       smem_desc(b_base + kk * (MMA_K / 2), 16, 1024, 2), idesc, sfa_addr,
-                       sfb_addr, (kb > 0 || kk > 0) ? 1u : 0u);
-          };
-          if (n_mma == BK / MMA_K) {
-#pragma unroll
-            for (int kk = 0; kk < BK / MMA_K; ++kk) step(kk);
-          } else {
-            for (int kk = 0; kk < n_mma; ++kk) step(kk);
-          }
-          issued = true;
-          tc_commit(empty_bar(s));
-        }
-        if (!ok) break;
-        tc_commit(acc_full);
-      }
-      if (issued) {
-        tc_commit(drain_bar);
-        volatile int no_abort = 0;
-        mbar_wait(drain_bar, 0, &no_abort, p.status, 0x3600);
-      }
-    }
-  } else if (warp >= EPI_WARP0 && warp < EPI_WARP0 + EPI_WARPS) {
+  } else if (warp < EPI_WARP0 + EPI_WARPS) {
+    if constexpr (EPI) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     // ------------------------------------------------------------ epilogue
     const float scale = p.alpha * (*p.a_sdec) * (*p.b_sdec);
     const int esize = p.out_mode == 1 ? 4 : 2;
@@ -371,22 +317,33 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
       const int64_t col = (int64_t)nb * BN + c_begin;
       const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)c_begin;
       if constexpr (EPI) {
-        // four 32-column blocks, one tensor-memory load each
+        // The whole row half leaves tensor memory first; then four 32-column
+        // blocks, each through the same 32 registers (the rest moves down: 96
+        // moves against some 600 instructions a block, and a quarter of the
+        // code, which an unrolled loop would stream through the instruction
+        // caches).
         uint32_t scales4 = 0;
-#pragma unroll 1
-        for (int h = 0; h < 4; ++h) {
-          uint32_t r[32];
-          tmem_ld32(taddr + 32 * h, r);
-          if (h == 3) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty);
-          }
-          if (ncols > 0) {
-            float v[32];
+        float v[128];
+        {
+          uint32_t r[128];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(__uint_as_float(r[i]), scale);
-            scales4 |= epilogue32(p, row, col + 32 * h, v, amax) << (8 * h);
+          for (int h = 0; h < 4; ++h) tmem_ld32_nowait(taddr + 32 * h, r + 32 * h);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(acc_empty);
+#pragma unroll
+          for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
+        }
+        if (ncols > 0) {
+#pragma unroll 1
+          for (int h = 0; h < 4; ++h) {
+            float u[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) u[i] = __fmul_rn(v[i], scale);
+            scales4 |= epilogue32(p, row, col + 32 * h, u, wide_st, amax) << (8 * h);
+#pragma unroll
+            for (int i = 0; i < 96; ++i) v[i] = v[i + 32];
           }
         }
         if (p.z_codes != nullptr && ncols > 0) {
@@ -560,6 +517,103 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
       for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
       if (lane == 0) atomicMax(reinterpret_cast<unsigned int*>(p.c_amax), __float_as_uint(amax));
     }
+  } else {
+    fewer_registers<EPI>();
+    if (warp == PRODUCER_WARP) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_b)) : "memory");
+      uint32_t it = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x) {
+        int mb, nb;
+        tile_coords(tile, tiles_m, tiles_n, mb, nb);
+        const bool b_hi = (nb * 2 + 1) * 128 < p.N;
+        for (int kb = 0; kb < k_blocks; ++kb, ++it) {
+          const int s = it % STAGES;
+          const uint32_t ph = (it / STAGES) & 1u;
+          if (!mbar_wait(empty_bar(s), ph ^ 1u, abort_flag, p.status, 0x3100 + s)) { ok = false; break; }
+          const int n_atoms = NV ? min(4, apr - kb * 4) : min(2, apr - kb * 2);
+          const uint32_t atom_bytes = (uint32_t)n_atoms * 512u;
+          // scale atoms first, on their own barrier: the stagers move them into
+          // tensor memory while the operand tiles are still in flight
+          mbar_arrive_expect_tx(atoms_bar(s), atom_bytes * (b_hi ? 3u : 2u));
+          const int atom0 = kb * (NV ? 4 : 2);
+          bulk_load(smem_u32(sSFA(s)), p.a_sf + ((size_t)mb * apr + atom0) * 512, atom_bytes,
+                    atoms_bar(s));
+          bulk_load(smem_u32(sSFB(s)), p.b_sf + ((size_t)(2 * nb) * apr + atom0) * 512, atom_bytes,
+                    atoms_bar(s));
+          if (b_hi)
+            bulk_load(smem_u32(sSFB(s) + 4 * 512), p.b_sf + ((size_t)(2 * nb + 1) * apr + atom0) * 512,
+                      atom_bytes, atoms_bar(s));
+          mbar_arrive_expect_tx(full_bar(s), A_BYTES + B_BYTES);
+          tma_load_2d(smem_u32(sA(s)), &tmap_a, full_bar(s), kb * (BK / 2), mb * BM);
+          tma_load_2d(smem_u32(sB(s)), &tmap_b, full_bar(s), kb * (BK / 2), nb * BN);
+        }
+      }
+      if (it > 0) {
+        const uint32_t first = it > (uint32_t)STAGES ? it - STAGES : 0;
+        for (uint32_t j = first; j < it; ++j) {
+          volatile int no_abort = 0;
+          mbar_wait(atoms_bar(j % STAGES), (j / STAGES) & 1u, &no_abort, p.status, 0x3200 + j % STAGES);
+          mbar_wait(full_bar(j % STAGES), (j / STAGES) & 1u, &no_abort, p.status, 0x3200 + j % STAGES);
+        }
+      }
+    }
+    } else if (warp == MMA_WARP) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      uint32_t it = 0, tile_iter = 0;
+      bool ok = true, issued = false;
+      for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x, ++tile_iter) {
+        if (!mbar_wait(acc_empty, (tile_iter & 1u) ^ 1u, abort_flag, p.status, 0x3400)) { ok = false; break; }
+        tc_fence_after();
+        for (int kb = 0; kb < k_blocks; ++kb, ++it) {
+          const int s = it % STAGES;
+          const uint32_t ph = (it / STAGES) & 1u;
+          if (!mbar_wait(sf_bar(s), ph, abort_flag, p.status, 0x3500 + s)) { ok = false; break; }
+          if (!mbar_wait(full_bar(s), ph, abort_flag, p.status, 0x3580 + s)) { ok = false; break; }
+          tc_fence_after();
+          const int n_mma = min(BK / MMA_K, (p.K - kb * BK) / MMA_K);
+          const uint32_t t_sfa = tmem_base + TMEM_SF_BASE + s * TMEM_SF_STAGE;
+          const uint32_t t_sfb = t_sfa + 16;
+          const uint32_t a_base = smem_u32(sA(s)), b_base = smem_u32(sB(s));
+          auto step = [&](int kk) {
+            uint32_t sfa_addr, sfb_addr, idesc;
+            if (NV) {
+              sfa_addr = t_sfa + 4 * kk;
+              sfb_addr = t_sfb + 8 * kk;
+              idesc = make_idesc(BN, BM, 0u, 0u, 0u);
+            } else {
+              const uint32_t byte = (uint32_t)(kk & 1) * 2u;
+              sfa_addr = (t_sfa + 4 * (kk >> 1)) | (byte << 30);
+              sfb_addr = (t_sfb + 8 * (kk >> 1)) | (byte << 30);
+              idesc = make_idesc(BN, BM, 1u, byte, byte);
+            }
+            tc_mma<NV>(tmem_base, smem_desc(a_base + kk * (MMA_K / 2), 16, 1024, 2),
+                       smem_desc(b_base + kk * (MMA_K / 2), 16, 1024, 2), idesc, sfa_addr,
+                       sfb_addr, (kb > 0 || kk > 0) ? 1u : 0u);
+          };
+          if (n_mma == BK / MMA_K) {
+#pragma unroll
+            for (int kk = 0; kk < BK / MMA_K; ++kk) step(kk);
+          } else {
+            for (int kk = 0; kk < n_mma; ++kk) step(kk);
+          }
+          issued = true;
+          tc_commit(empty_bar(s));
+        }
+        if (!ok) break;
+        tc_commit(acc_full);
+      }
+      if (issued) {
+        tc_commit(drain_bar);
+        volatile int no_abort = 0;
+        mbar_wait(drain_bar, 0, &no_abort, p.status, 0x3600);
+      }
+    }
+    }
   }
 
   tc_fence_before();
@@ -618,7 +672,7 @@ fp4_status gemm_launch(const GemmArgs& g, cudaStream_t s) {
   p.q_sr = g.q_sr; p.q_stream = g.q_stream; p.q_keys = fp4dev::philox_keys(g.q_seed);
   p.act = g.act; p.bias = g.bias; p.bias_f32 = g.bias_f32;
   p.res = g.res; p.ldr = g.ldr; p.res_f32 = g.res_f32;
-  p.z_codes = g.z_codes; p.z_scales = g.z_scales;
+  p.z_codes = g.z_codes; p.z_scales = g.z_scales; p.z_wide = ptr_aligned(g.z_codes, 32);
   p.c_amax = g.c_amax; p.status = g.status;
   const int tiles = (int)(g.M / BM) * (int)((g.N + BN - 1) / BN);
   const int grid = tiles < sm_count() ? tiles : sm_count();

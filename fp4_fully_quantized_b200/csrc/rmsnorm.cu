@@ -312,7 +312,7 @@ fp4_status fqt_rmsnorm_fwd(const void* x, int64_t ldx, const void* residual, int
                            float* y_amax, void* ws, size_t ws_bytes, void* stream) {
   fp4_status st = check_norm(rows, cols, weight, w_dtype, ws, ws_bytes);
   if (st != FP4_OK) return st;
-  if (y == nullptr && q8 == nullptr) return FP4_ERR_NULL;
+  if (y == nullptr && q8 == nullptr && rows > 0) return FP4_ERR_NULL;
   if ((residual == nullptr) != (res_out == nullptr) && rows > 0) return FP4_ERR_NULL;
   if (!(eps > 0.0f) || !(eps <= FLT_MAX)) return FP4_ERR_FORMAT;
   if (residual != nullptr && !known_dtype(res_dtype)) return FP4_ERR_FORMAT;

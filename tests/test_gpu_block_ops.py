@@ -133,7 +133,9 @@ def test_no_rows(gpu_lib):
     F.fqt_rmsnorm_fwd(e(64), one(64), e(64), q8=F.Ckpt8.empty(0, 64), rstd=one(0), y_amax=amax)
     F.fqt_rmsnorm_bwd(e(64), one(64), one(0), e(64), s=e(64), dweight=dw)
     assert float(amax) == 0 and (dw == 0).all()
+    F.fqt_rmsnorm_fwd(e(64), one(64), e(64))
     amax.fill_(3)
+    F.fqt_act_fwd(e(128), e(64), gated=True)
     F.fqt_act_fwd(e(128), e(64), gated=True, z8=F.Ckpt8.empty(0, 128))
     F.fqt_act_bwd(e(64), F.Ckpt8.empty(0, 128), e(128), gated=True, dbias=db, dz_amax=amax)
     assert float(amax) == 0 and (db == 0).all()
