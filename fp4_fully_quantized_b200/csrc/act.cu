@@ -76,9 +76,11 @@ __global__ void __launch_bounds__(kThreads) act_fwd_kernel(const ActParams p) {
     if (p.out != nullptr && ok) {
       float y[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y[i] = act_value<ACT>(g[i]);
-        if constexpr (GATED) y[i] *= u[i];
+      for (int i = 0; i < 8; i += 2) {
+        y[i] = g[i];
+        y[i + 1] = g[i + 1];
+        act_value2<ACT>(y[i], y[i + 1]);
+        if constexpr (GATED) { y[i] *= u[i]; y[i + 1] *= u[i + 1]; }
       }
       const uint4 packed = pack_bf16x8(y);
       *reinterpret_cast<uint4*>(p.out + row * p.ldo + c) = packed;
@@ -116,22 +118,26 @@ __global__ void __launch_bounds__(kThreads) act_bwd_kernel(const ActParams p) {
       float u[8], du[8];
       load_z<CKPT>(p, row, p.cols + c, u);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float f, df;
-        act_both<ACT>(g[i], f, df);
-        d[i] = dy[i] * u[i] * df;
-        du[i] = dy[i] * f;
-        db[8 + i] += du[i];
+      for (int i = 0; i < 8; i += 2) {
+        float f[2], df[2];
+        act_both2<ACT>(g[i], g[i + 1], f[0], f[1], df[0], df[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          d[i + j] = dy[i + j] * u[i + j] * df[j];
+          du[i + j] = dy[i + j] * f[j];
+          db[8 + i + j] += du[i + j];
+        }
       }
       const uint4 packed = pack_bf16x8(du);
       *reinterpret_cast<uint4*>(p.out + row * p.ldo + p.cols + c) = packed;
       amax = max(amax, amax_bits_bf16x8(packed));
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float f, df;
-        act_both<ACT>(g[i], f, df);
-        d[i] = dy[i] * df;
+      for (int i = 0; i < 8; i += 2) {
+        float f[2], df[2];
+        act_both2<ACT>(g[i], g[i + 1], f[0], f[1], df[0], df[1]);
+        d[i] = dy[i] * df[0];
+        d[i + 1] = dy[i + 1] * df[1];
       }
     }
 #pragma unroll

@@ -71,49 +71,78 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 // ---------------------------------------------------------------------------
 // Activations.  silu(z) = z p, p = 1 / (1 + exp(-z)); gelu(z) = z Phi(z) with
 // the normal CDF Phi; gelu_tanh(z) = z (1 + tanh u) / 2 = z p(2u),
-// u = sqrt(2/pi) (z + 0.044715 z^3).  The exponential and the quotient are the
-// fast forms (relative error about 2^-21 over the range where p matters,
-// against 2^-9 of the BF16 result).  z^2 is capped in gelu_tanh where p is
-// 0 or 1 in binary32 anyway, so that a large z does not meet Inf * 0.
+// u = sqrt(2/pi) (z + 0.044715 z^3).  Exponential and reciprocal are the
+// hardware's approximations (2 and 1 units in the last place, subnormals
+// flushed), against 2^-9 of a BF16 result.  z^2 is capped in gelu_tanh where p
+// is 0 or 1 in binary32 anyway, so that a large z does not meet Inf * 0.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+__device__ __forceinline__ float ex2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float logistic(float z) { return rcp_approx(1.0f + ex2_approx(-kLog2e * z)); }
 
-// The normal CDF and e = exp(-z^2/2), by the rational approximation of erfc of
-// Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26: for x >= 0
+// The upper normal tail Q(a) = 1 - Phi(a) and e = exp(-a^2/2) at a = min(|z|, 14)
+// for two values, by the rational approximation of erfc of Abramowitz and
+// Stegun, Handbook of Mathematical Functions, 7.1.26: for x >= 0
 // erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), to
-// 1.5e-7, with x = |z| / sqrt(2) (so the exponential is the density's too, and
-// the lower tail is not a difference).  An absolute error of 0.75e-7 is one
-// and a quarter units of FP32's last place at 1.
-__device__ __forceinline__ float normal_cdf(float z, float& e) {
-  const float t = __fdividef(1.0f, 1.0f + 0.23164190f * fabsf(z));   // 0.3275911 / sqrt(2)
-  e = __expf(-0.5f * z * z);
-  float q = 1.061405429f;
-  q = q * t - 1.453152027f;
-  q = q * t + 1.421413741f;
-  q = q * t - 0.284496736f;
-  q = q * t + 0.254829592f;
-  const float tail = 0.5f * (q * t) * e;
-  return z < 0.0f ? tail : 1.0f - tail;
+// 1.5e-7, with x = a / sqrt(2): the exponential is the density's too.  An error
+// of 0.75e-7 is one and a quarter units of FP32's last place at 1.  Both
+// reciprocals come from one (of the product: at most 18), because the special
+// functions' pipe, a quarter as wide as the FMA's, would be the bound.
+__device__ __forceinline__ void normal_tail2(float z0, float z1, float& a0, float& a1, float& q0,
+                                             float& q1, float& e0, float& e1) {
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(a0) : "f"(fabsf(z0)), "f"(14.0f));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(a1) : "f"(fabsf(z1)), "f"(14.0f));
+  const float d0 = 1.0f + 0.23164190f * a0, d1 = 1.0f + 0.23164190f * a1;   // 0.3275911 / sqrt(2)
+  const float r = rcp_approx(d0 * d1);
+  const float t0 = r * d1, t1 = r * d0;
+  e0 = ex2_approx((-0.5f * kLog2e) * a0 * a0);
+  e1 = ex2_approx((-0.5f * kLog2e) * a1 * a1);
+  const auto poly = [](float t) {            // half of a1 t + ... + a5 t^5
+    float q = 0.5f * 1.061405429f;
+    q = q * t - 0.5f * 1.453152027f;
+    q = q * t + 0.5f * 1.421413741f;
+    q = q * t - 0.5f * 0.284496736f;
+    q = q * t + 0.5f * 0.254829592f;
+    return q * t;
+  };
+  q0 = poly(t0) * e0;
+  q1 = poly(t1) * e1;
 }
 
 constexpr float kTwoC = 1.5957691216057308f;          // 2 sqrt(2/pi)
 
 template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-  if constexpr (ACT == FQT_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
-  if constexpr (ACT == FQT_ACT_SILU) return z * logistic(z);
+__device__ __forceinline__ void act_both(float z, float& f, float& df);
+
+// The values at z0 and z1, in place.
+template <int ACT>
+__device__ __forceinline__ void act_value2(float& z0, float& z1) {
   if constexpr (ACT == FQT_ACT_GELU) {
-    float e;
-    return z * normal_cdf(z, e);
+    // z Phi(z) = max(z, 0) - |z| Q(|z|)
+    float a0, a1, q0, q1, e0, e1;
+    normal_tail2(z0, z1, a0, a1, q0, q1, e0, e1);
+    z0 = fmaxf(z0, 0.0f) - a0 * q0;
+    z1 = fmaxf(z1, 0.0f) - a1 * q1;
+  } else {
+    float d;
+    act_both<ACT>(z0, z0, d);
+    act_both<ACT>(z1, z1, d);
   }
-  if constexpr (ACT == FQT_ACT_GELU_TANH)
-    return z * logistic(kTwoC * z * (1.0f + 0.044715f * fminf(z * z, 1e4f)));
-  return z;
 }
 
-// The value and the derivative at z.
+// The value and the derivative at z (not GELU).
 template <int ACT>
 __device__ __forceinline__ void act_both(float z, float& f, float& df) {
+  static_assert(ACT != FQT_ACT_GELU, "in pairs: act_both2");
   if constexpr (ACT == FQT_ACT_NONE) { f = z; df = 1.0f; }
   if constexpr (ACT == FQT_ACT_RELU) {
     f = z > 0.0f ? z : (z != z ? z : 0.0f);
@@ -124,17 +153,29 @@ __device__ __forceinline__ void act_both(float z, float& f, float& df) {
     f = z * p;
     df = p + f * (1.0f - p);
   }
-  if constexpr (ACT == FQT_ACT_GELU) {
-    float e;
-    const float cdf = normal_cdf(z, e);
-    f = z * cdf;
-    df = cdf + z * (0.3989422804014327f * e);
-  }
   if constexpr (ACT == FQT_ACT_GELU_TANH) {
     const float z2 = fminf(z * z, 1e4f);
     const float p = logistic(kTwoC * z * (1.0f + 0.044715f * z2));
     f = z * p;
     df = p + f * (1.0f - p) * (kTwoC * (1.0f + 0.134145f * z2));
+  }
+}
+
+// Values and derivatives at z0 and z1.
+template <int ACT>
+__device__ __forceinline__ void act_both2(float z0, float z1, float& f0, float& f1, float& df0,
+                                          float& df1) {
+  if constexpr (ACT == FQT_ACT_GELU) {
+    // Phi + z phi: beyond |z| = 14 the second term is below 2^-126
+    float a0, a1, q0, q1, e0, e1;
+    normal_tail2(z0, z1, a0, a1, q0, q1, e0, e1);
+    f0 = fmaxf(z0, 0.0f) - a0 * q0;
+    f1 = fmaxf(z1, 0.0f) - a1 * q1;
+    df0 = (z0 < 0.0f ? q0 : 1.0f - q0) + copysignf(a0, z0) * (0.3989422804014327f * e0);
+    df1 = (z1 < 0.0f ? q1 : 1.0f - q1) + copysignf(a1, z1) * (0.3989422804014327f * e1);
+  } else {
+    act_both<ACT>(z0, f0, df0);
+    act_both<ACT>(z1, f1, df1);
   }
 }
 

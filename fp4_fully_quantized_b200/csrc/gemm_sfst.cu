@@ -46,13 +46,14 @@ constexpr int SFA_BYTES = 4 * 512;
 constexpr int SFB_BYTES = 2 * 4 * 512;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 256;
+constexpr int EPI_SMEM_BYTES = SMEM_BYTES + 8 * 128 * 4;   // and the epilogue warps' bias values
 constexpr int NUM_THREADS = 512;
 constexpr int SF_WARP0 = 0, EPI_WARP0 = 4, EPI_WARPS = 8, PRODUCER_WARP = 12, MMA_WARP = 13;
 constexpr int TMEM_COLS = 512;
 constexpr int TMEM_SF_BASE = 256;
 constexpr int TMEM_SF_STAGE = 48;             // 16 (A) + 32 (B) columns per stage
 static_assert(TMEM_SF_BASE + STAGES * TMEM_SF_STAGE <= TMEM_COLS, "TMEM budget");
-static_assert(SMEM_BYTES <= 232448, "shared-memory budget");
+static_assert(EPI_SMEM_BYTES <= 232448, "shared-memory budget");
 
 struct StParams {
   const uint8_t* a_sf; const uint8_t* b_sf;
@@ -70,7 +71,7 @@ struct StParams {
   // EPI kernels: bias, activation, residual, 8-bit checkpoint
   int act;
   const void* bias; bool bias_f32;
-  const void* res; int64_t ldr; bool res_f32;
+  const void* res; int64_t ldr; bool res_f32; bool res_wide;   // rows 32-byte aligned
   uint8_t* z_codes; uint8_t* z_scales; bool z_wide;   // codes 32-byte aligned
   uint32_t* status;
 };
@@ -105,19 +106,38 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 template <int ACT>
 __device__ __forceinline__ void act32(float* v) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = fp4dev::act_value<ACT>(v[i]);
+  for (int i = 0; i < 32; i += 2) fp4dev::act_value2<ACT>(v[i], v[i + 1]);
 }
 
+// 64 bytes of a residual row from column `col`: 32 BF16 or 16 FP32 values.
+__device__ __forceinline__ void load_residual(const StParams& p, int64_t row, int64_t col, uint32_t* r) {
+  const char* src = static_cast<const char*>(p.res) + (row * p.ldr + col) * (p.res_f32 ? 4 : 2);
+  if (p.res_wide) {
+    ld_global_v8(src, r);
+    ld_global_v8(src + 32, r + 8);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 x = reinterpret_cast<const uint4*>(src)[i];
+      r[4 * i] = x.x; r[4 * i + 1] = x.y; r[4 * i + 2] = x.z; r[4 * i + 3] = x.w;
+    }
+  }
+}
+
+// `bias`: its 32 values in shared memory; `r`: the residual's first 64 bytes,
+// replaced by those 32 columns on when `more`.
 __device__ __forceinline__ uint32_t epilogue32(const StParams& p, int64_t row, int64_t col, float* v,
+                                               const float* bias, uint32_t* r, bool more,
                                                bool wide_st, float& amax) {
   uint32_t byte = 0;
   if (p.bias != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-      float b[8];
-      fp4dev::load8(p.bias, col + i, p.bias_f32, b);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i + j] = __fadd_rn(v[i + j], b[j]);   // no FMA: z is fp4_gemm's P + bias
+    for (int i = 0; i < 32; i += 4) {        // __fadd_rn: no FMA, z is fp4_gemm's P + bias
+      const float4 b = *reinterpret_cast<const float4*>(bias + i);
+      v[i] = __fadd_rn(v[i], b.x);
+      v[i + 1] = __fadd_rn(v[i + 1], b.y);
+      v[i + 2] = __fadd_rn(v[i + 2], b.z);
+      v[i + 3] = __fadd_rn(v[i + 3], b.w);
     }
   }
   if (p.z_codes != nullptr) {
@@ -147,13 +167,20 @@ __device__ __forceinline__ uint32_t epilogue32(const StParams& p, int64_t row, i
     default: break;
   }
   if (p.res != nullptr) {
+    if (p.res_f32) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-      float r[8];
-      fp4dev::load8(p.res, row * p.ldr + col + i, p.res_f32, r);
+      for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(r[i]);
+      load_residual(p, row, col + 16, r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i + j] += r[j];
+      for (int i = 0; i < 16; ++i) v[16 + i] += __uint_as_float(r[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        v[2 * i] += __uint_as_float(r[i] << 16);
+        v[2 * i + 1] += __uint_as_float(r[i] & 0xFFFF0000u);
+      }
     }
+    if (more) load_residual(p, row, col + 32, r);
   }
   if (p.c_amax != nullptr) {
 #pragma unroll
@@ -190,7 +217,7 @@ __device__ __forceinline__ uint32_t epilogue32(const StParams& p, int64_t row, i
 // hold a row's 128 accumulator columns at once, so that the accumulator is free
 // for the next tile's MMAs before any of the epilogue's arithmetic.  The sum is
 // what the 512 threads are launched with, 4 x 128.
-constexpr int kEpiRegs = 184, kOtherRegs = 72;
+constexpr int kEpiRegs = 192, kOtherRegs = 64;
 static_assert(2 * kEpiRegs + 2 * kOtherRegs <= 4 * 128, "register split");
 template <bool EPI>
 __device__ __forceinline__ void fewer_registers() {
@@ -306,22 +333,47 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
     float amax = 0.0f;
     uint32_t tile_iter = 0;
     const int quad = warp & 3, half = (warp - EPI_WARP0) >> 2;
+    const int c_begin = half * (BN / 2);
+    // EPI: this warp's 128 bias values, as FP32
+    float* const bias_s = reinterpret_cast<float*>(base + STAGES * STAGE_BYTES + 256) + (warp - EPI_WARP0) * 128;
     for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++tile_iter) {
-      if (!warp_wait(acc_full, tile_iter & 1u, abort_flag, p.status, 0x3700 + warp, lane)) break;
-      tc_fence_after();
       int mb, nb;
       tile_coords(tile, tiles_m, tiles_n, mb, nb);
       const int64_t row = (int64_t)mb * BM + quad * 32 + lane;
-      const int c_begin = half * (BN / 2);
       const int ncols = min(BN / 2, p.N - nb * BN - c_begin);
       const int64_t col = (int64_t)nb * BN + c_begin;
+      uint32_t res[16];
+      if constexpr (EPI) {
+        // what the tile needs besides its accumulator, before the wait for that
+        if (ncols > 0 && p.bias != nullptr) {
+          __syncwarp();                     // the last tile's values have been read
+          float4 b;
+          const int64_t at = col + 4 * lane;
+          if (p.bias_f32) {
+            b = *reinterpret_cast<const float4*>(static_cast<const float*>(p.bias) + at);
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.bias) + at);
+            b = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u),
+                            __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xFFFF0000u));
+          }
+          reinterpret_cast<float4*>(bias_s)[lane] = b;
+          __syncwarp();
+        }
+        if (ncols > 0 && p.res != nullptr) {
+          load_residual(p, row, col, res);
+          // the rest of its row towards L2
+          const char* src = static_cast<const char*>(p.res) + (row * p.ldr + col) * (p.res_f32 ? 4 : 2);
+          const int bytes = 128 * (p.res_f32 ? 4 : 2);
+          for (int o = 128; o < bytes; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + o));
+        }
+      }
+      if (!warp_wait(acc_full, tile_iter & 1u, abort_flag, p.status, 0x3700 + warp, lane)) break;
+      tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)c_begin;
       if constexpr (EPI) {
-        // The whole row half leaves tensor memory first; then four 32-column
-        // blocks, each through the same 32 registers (the rest moves down: 96
-        // moves against some 600 instructions a block, and a quarter of the
-        // code, which an unrolled loop would stream through the instruction
-        // caches).
+        // The whole row half leaves tensor memory first; then four blocks of 32
+        // columns, two to an iteration: of one, two and four that measured
+        // fastest (fewer moves of the rest than one, less code than four).
         uint32_t scales4 = 0;
         float v[128];
         {
@@ -337,13 +389,16 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
         }
         if (ncols > 0) {
 #pragma unroll 1
-          for (int h = 0; h < 4; ++h) {
-            float u[32];
+          for (int h = 0; h < 4; h += 2) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) u[i] = __fmul_rn(v[i], scale);
-            scales4 |= epilogue32(p, row, col + 32 * h, u, wide_st, amax) << (8 * h);
+            for (int k = 0; k < 2; ++k) {
 #pragma unroll
-            for (int i = 0; i < 96; ++i) v[i] = v[i + 32];
+              for (int i = 0; i < 32; ++i) v[32 * k + i] = __fmul_rn(v[32 * k + i], scale);
+              scales4 |= epilogue32(p, row, col + 32 * (h + k), v + 32 * k, bias_s + 32 * (h + k), res,
+                                    h + k < 3, wide_st, amax) << (8 * (h + k));
+            }
+#pragma unroll
+            for (int i = 0; i < 64; ++i) v[i] = v[i + 64];
           }
         }
         if (p.z_codes != nullptr && ncols > 0) {
@@ -672,6 +727,7 @@ fp4_status gemm_launch(const GemmArgs& g, cudaStream_t s) {
   p.q_sr = g.q_sr; p.q_stream = g.q_stream; p.q_keys = fp4dev::philox_keys(g.q_seed);
   p.act = g.act; p.bias = g.bias; p.bias_f32 = g.bias_f32;
   p.res = g.res; p.ldr = g.ldr; p.res_f32 = g.res_f32;
+  p.res_wide = ptr_aligned(g.res, 32) && (g.ldr * (g.res_f32 ? 4 : 2)) % 32 == 0;
   p.z_codes = g.z_codes; p.z_scales = g.z_scales; p.z_wide = ptr_aligned(g.z_codes, 32);
   p.c_amax = g.c_amax; p.status = g.status;
   const int tiles = (int)(g.M / BM) * (int)((g.N + BN - 1) / BN);
@@ -680,9 +736,10 @@ fp4_status gemm_launch(const GemmArgs& g, cudaStream_t s) {
     return FP4_ERR_CUDA;
   const auto kernel = g.epi ? (nv ? fp4_gemm_sfst_kernel<true, true> : fp4_gemm_sfst_kernel<false, true>)
                             : (nv ? fp4_gemm_sfst_kernel<true, false> : fp4_gemm_sfst_kernel<false, false>);
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess)
+  const int smem = g.epi ? EPI_SMEM_BYTES : SMEM_BYTES;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return FP4_ERR_CUDA;
-  kernel<<<grid, NUM_THREADS, SMEM_BYTES, s>>>(ta, tb, p);
+  kernel<<<grid, NUM_THREADS, smem, s>>>(ta, tb, p);
   count_launches(1);
   return cudaGetLastError() == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }
