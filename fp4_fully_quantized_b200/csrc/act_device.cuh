@@ -238,9 +238,8 @@ __device__ __forceinline__ void store8(void* base, int64_t i, bool f32, const fl
 // A thread's eight values of a 32-column block (four neighbouring lanes hold it;
 // every lane of the warp calls this) to E4M3; false for a block with Inf or NaN.
 __device__ __forceinline__ bool encode8(const float* v, uint8_t* codes, uint8_t* scale, bool valid) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+  uint32_t m = abs_bits(max_abs3(max_abs3(max_abs3(max_abs3(0.0f, v[0], v[1]), v[2], v[3]), v[4], v[5]),
+                                 v[6], v[7]));
   m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
   m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
   const uint32_t byte = ckpt_scale_byte(m);
@@ -249,6 +248,115 @@ __device__ __forceinline__ bool encode8(const float* v, uint8_t* codes, uint8_t*
     *reinterpret_cast<uint2*>(codes) =
         make_uint2(e4m3x4_rn(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
                    e4m3x4_rn(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+    if ((threadIdx.x & 3) == 0) *scale = (uint8_t)byte;
+  }
+  return byte != kCkptNanScale;
+}
+
+// ---------------------------------------------------------------------------
+// Eight consecutive FP32 values as four pairs: one instruction multiplies or adds
+// two of them (fma.rn.f32x2), each rounded as the scalar form rounds it.  The
+// kernels that use this are bound by instruction issue where they are not bound
+// by HBM.
+// ---------------------------------------------------------------------------
+typedef unsigned long long f32x2;
+struct F8 { f32x2 p[4]; };
+
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F8 zero8() { return F8{{0ull, 0ull, 0ull, 0ull}}; }
+__device__ __forceinline__ F8 scaled8(const F8& v, float k) {
+  const f32x2 kk = pair(k, k);
+  return F8{{mul2(v.p[0], kk), mul2(v.p[1], kk), mul2(v.p[2], kk), mul2(v.p[3], kk)}};
+}
+
+__device__ __forceinline__ F8 bf16x8(const uint4& u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  F8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r.p[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  return r;
+}
+__device__ __forceinline__ F8 e4m3x8(const uint2& q) {
+  F8 r;
+  float v[4];
+  e4m3x4_to_f32(q.x, v);
+  r.p[0] = pair(v[0], v[1]);
+  r.p[1] = pair(v[2], v[3]);
+  e4m3x4_to_f32(q.y, v);
+  r.p[2] = pair(v[0], v[1]);
+  r.p[3] = pair(v[2], v[3]);
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ F8 get8(const void* base, int64_t i) {
+  if constexpr (F32) {
+    const ulonglong2* p = reinterpret_cast<const ulonglong2*>(static_cast<const float*>(base) + i);
+    const ulonglong2 a = p[0], b = p[1];
+    return F8{{a.x, a.y, b.x, b.y}};
+  } else {
+    return bf16x8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + i));
+  }
+}
+__device__ __forceinline__ uint4 pack_bf16x8(const F8& v) {
+  uint4 u;
+  float2 f = unpair(v.p[0]);
+  u.x = pack_bf16x2(f.x, f.y);
+  f = unpair(v.p[1]);
+  u.y = pack_bf16x2(f.x, f.y);
+  f = unpair(v.p[2]);
+  u.z = pack_bf16x2(f.x, f.y);
+  f = unpair(v.p[3]);
+  u.w = pack_bf16x2(f.x, f.y);
+  return u;
+}
+template <bool F32>
+__device__ __forceinline__ void put8(void* base, int64_t i, const F8& v) {
+  if constexpr (F32) {
+    ulonglong2* p = reinterpret_cast<ulonglong2*>(static_cast<float*>(base) + i);
+    p[0] = make_ulonglong2(v.p[0], v.p[1]);
+    p[1] = make_ulonglong2(v.p[2], v.p[3]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + i) = pack_bf16x8(v);
+  }
+}
+
+// A thread's eight values of a 32-column block (four neighbouring lanes hold it;
+// every lane of the warp calls this) to E4M3; false for a block with Inf or NaN.
+__device__ __forceinline__ bool encode8(const F8& x, uint8_t* codes, uint8_t* scale, bool valid) {
+  const float2 a = unpair(x.p[0]), b = unpair(x.p[1]), c = unpair(x.p[2]), d = unpair(x.p[3]);
+  uint32_t m = abs_bits(max_abs3(max_abs3(max_abs3(max_abs3(0.0f, a.x, a.y), b.x, b.y), c.x, c.y), d.x, d.y));
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  const uint32_t byte = ckpt_scale_byte(m);
+  if (valid) {
+    const F8 v = scaled8(x, ckpt_inv_scale(byte));
+    const float2 e = unpair(v.p[0]), f = unpair(v.p[1]), g = unpair(v.p[2]), h = unpair(v.p[3]);
+    *reinterpret_cast<uint2*>(codes) = make_uint2(e4m3x4_rn(e.x, e.y, f.x, f.y), e4m3x4_rn(g.x, g.y, h.x, h.y));
     if ((threadIdx.x & 3) == 0) *scale = (uint8_t)byte;
   }
   return byte != kCkptNanScale;

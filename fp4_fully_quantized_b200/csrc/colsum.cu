@@ -2,9 +2,9 @@
 // row slices' partial sums, and the size helpers of these calls' buffers.
 //
 // out[c] = sum over the slices of partial[slice][c], slice order fixed.  The
-// partials (at most 296 rows) were just written and are in L2; the kernel is
+// partials (at most 444 rows) were just written and are in L2; the kernel is
 // bound by the latency of its loads, so 32 threads share a column's slices
-// (at most 10 loads each, all in flight together) and join through shared
+// (at most 14 loads each, all in flight together) and join through shared
 // memory; a CTA covers 32 columns, one 128-byte line of each slice.
 #include <cuda_runtime.h>
 

@@ -84,7 +84,7 @@ cudaError_t launch_quant_2d(const Quant2DArgs& a, cudaStream_t s);
 // Kernels that sum over rows (dweight, dbias) write one partial row of sums per
 // row slice behind the status block of the workspace; launch_colsum adds the
 // slices in order, so a result's additions depend on the shape alone.
-constexpr int kMaxSlices = 296;      // two CTAs on each of 148 SMs
+constexpr int kMaxSlices = 444;      // three CTAs on each of 148 SMs
 inline int64_t colsum_slices(int64_t rows) { return rows < kMaxSlices ? rows : kMaxSlices; }
 inline float* colsum_partials(void* ws) {
   return reinterpret_cast<float*>(static_cast<char*>(ws) + sizeof(DeviceStatus));

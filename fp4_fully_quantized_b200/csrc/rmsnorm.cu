@@ -8,26 +8,33 @@
 // dres; dweight sums dy * xhat over the rows in registers, one partial row per
 // CTA, joined by colsum.cu.
 //
-// A row belongs to a group of threads, each of which holds V chunks of eight
-// consecutive columns, the group's threads side by side: 8, 16 or 32 lanes of
-// a warp for rows of up to 1024 columns (several rows per CTA, no barrier), a
-// CTA for longer ones.  Both kernels are bound by HBM.
+// Both kernels are bound by HBM.  What that takes is bytes in flight while a
+// row's two phases (sum, then outputs) run, and few instructions a value:
+//  - persistent CTAs of independent thread groups, a row (or, below 33 threads,
+//    a few) to a group at a time, up to four chunks of eight columns to a thread
+//    (one chunk and four times the threads spent 1.4 us a row of 4096 on issue);
+//  - a group has a ring of bulk copies (cp.async.bulk onto an mbarrier) that
+//    brings its next rows to shared memory, and a barrier of its own, so that
+//    the groups of an SM are in different phases;
+//  - rows that fill their threads' chunks take a path without bounds.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
 #include "act_device.cuh"
 #include "fp4_device.cuh"
 #include "internal.h"
+#include "sm100_ptx.cuh"
 
 namespace fp4impl {
 using namespace fp4dev;
 namespace {
 
-constexpr int kMaxCols = 32768;      // 1024 threads x 4 chunks of 8
-constexpr int kGroupThreads = 256;   // CTA of the lane-group kernels
+constexpr int kMaxCols = 16384;      // 512 threads x 4 chunks of 8
+constexpr int kMaxStages = 8;
 
 struct FwdParams {
   const __nv_bfloat16* x; int64_t ldx;
@@ -38,6 +45,7 @@ struct FwdParams {
   __nv_bfloat16* y; int64_t ldy;
   uint8_t* codes; uint8_t* scales; bool q_xhat;
   float* rstd; float* y_amax; uint32_t* status;
+  int T, stages;
 };
 
 struct BwdParams {
@@ -48,88 +56,256 @@ struct BwdParams {
   const void* dres; int64_t lddres;
   void* dx; int64_t lddx; bool grad_f32;
   int64_t rows; int cols;
-  float* partial;
+  float* partial; uint32_t* status;
+  int T, stages;
 };
 
-// Sum over the group: G lanes of the warp, or (G == 0) the CTA through `slot`
-// (one float per warp; the caller alternates between two slots, so one barrier
-// per sum is enough).  Every thread gets the same value, added in a fixed order.
-template <int G>
-__device__ __forceinline__ float group_sum(float v, float* slot) {
-  constexpr int W = G == 0 ? 32 : G;
+// A group's ring: `stages` slots, each with up to three sources' rows of one
+// tile (the rows a group takes at a time).  Tile t of the group's sequence uses
+// slot t % stages.
+struct Source { const char* base; int64_t pitch; int row_bytes; };   // pitch in bytes
+
+template <int N>
+struct Ring {
+  Source src[N];
+  uint32_t bars, data;           // shared-memory addresses
+  int stages, stage_bytes, rows_per_tile;
+  int64_t rows;
+
+  // Called by the group's first warp: copies the rows of `tile` into `slot`.
+  // Rows that lie side by side in memory are one copy, others one each.
+  __device__ __forceinline__ void fetch(int64_t tile, int slot) const {
+    const int lane = threadIdx.x & 31;
+    const int64_t row0 = tile * rows_per_tile;
+    const int n = (int)(rows - row0 < rows_per_tile ? rows - row0 : rows_per_tile);
+    const uint32_t bar = bars + 8 * slot;
+    if (lane == 0) {
+      uint32_t bytes = 0;
+#pragma unroll
+      for (int j = 0; j < N; ++j) bytes += (uint32_t)(n * src[j].row_bytes);
+      ptx::mbar_arrive_expect_tx(bar, bytes);
+    }
+    __syncwarp();
+    uint32_t dst = data + slot * stage_bytes;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int bytes = src[j].row_bytes;
+      if (bytes != 0) {
+        const char* from = src[j].base + row0 * src[j].pitch;
+        if (src[j].pitch == bytes || rows_per_tile == 1) {
+          if (lane == 0) ptx::bulk_load(dst, from, (uint32_t)(n * bytes), bar);
+        } else {
+          for (int r = lane; r < n; r += 32)
+            ptx::bulk_load(dst + r * bytes, from + r * src[j].pitch, (uint32_t)bytes, bar);
+        }
+        dst += bytes * rows_per_tile;
+      }
+    }
+  }
+  // Bounded wait for a slot's copies.
+  __device__ __forceinline__ bool wait(int slot, uint32_t parity) const {
+    if (ptx::mbar_try_wait(bars + 8 * slot, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    while (!ptx::mbar_try_wait_sleep(bars + 8 * slot, parity))
+      if (ptx::globaltimer() - t0 > ptx::kWaitNs) return false;
+    return true;
+  }
+};
+
+// The group's barrier, with the OR of `flag` over its threads.
+__device__ __forceinline__ bool group_sync_or(int group, int threads, bool flag) {
+  if (threads == 32) {
+    __syncwarp();
+    return __any_sync(0xFFFFFFFFu, flag);
+  }
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %3, 0;\n\t"
+      "barrier.cta.red.or.pred p, %1, %2, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(any) : "r"(group + 1), "r"(threads), "r"((uint32_t)flag) : "memory");
+  return any != 0;
+}
+
+// Sum over the T threads of a row: W lanes of a warp (all of a row of up to 32
+// threads), then the row's warps through `slot`, one float a warp.  The group's
+// barrier is in here, whatever T is.  Every thread of the row gets the same
+// value, added in a fixed order.
+template <int W>
+__device__ __forceinline__ float row_sum(float v, float* slot, int T, int group, bool& failed) {
 #pragma unroll
   for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if constexpr (G == 0) {
-    if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
-    __syncthreads();
-    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-    v = lane < warps ? slot[lane] : 0.0f;
+  if (W < 32 || T == 32) {
+    failed = group_sync_or(group, 32, failed);
+  } else {
+    const int warps = T >> 5, lane = threadIdx.x & 31, i = lane & 15;     // at most 16 warps
+    if (lane == 0) slot[threadIdx.x >> 5] = v;
+    failed = group_sync_or(group, T, failed);
+    v = i < warps ? slot[group * warps + i] : 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   }
   return v;
 }
 
-// RES: 0 no residual, 1 BF16, 2 FP32.
-template <int G, int V, int RES>
-__global__ void __launch_bounds__(G ? kGroupThreads : 1024)
+// What both kernels set up: the barriers, each group's first copies, and the
+// weights as FP32 behind the rings.
+template <int N>
+__device__ __forceinline__ void ring_start(Ring<N>& ring, uint8_t* smem, uint64_t* bars, int stages,
+                                           int group, int groups, bool first_warp, int64_t tile0,
+                                           int64_t step, int64_t tiles, int cols, const void* w,
+                                           bool w_f32) {
+  ring.bars = ptx::smem_u32(bars + group * stages);
+  ring.data = ptx::smem_u32(smem) + group * stages * ring.stage_bytes;
+  ring.stages = stages;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < groups * stages; ++i) ptx::mbar_init(ptx::smem_u32(bars) + 8 * i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  __syncthreads();
+  if (first_warp)
+    for (int i = 0; i < stages; ++i)
+      if (tile0 + i * step < tiles) ring.fetch(tile0 + i * step, i);
+  float* const ws = reinterpret_cast<float*>(smem + groups * stages * ring.stage_bytes);
+  for (int c = threadIdx.x * 8; c < cols; c += blockDim.x * 8) {
+    float v[8];
+    load8(w, c, w_f32, v);
+    store8(ws, c, true, v);
+  }
+  __syncthreads();
+}
+
+// After a copy that did not arrive in time: wait for those still on their way,
+// so that none writes to shared memory that is no longer this CTA's.
+template <int N>
+__device__ __forceinline__ void ring_give_up(const Ring<N>& ring, int slot, uint32_t phase,
+                                             uint32_t* status, uint32_t where) {
+  set_status(status, FP4_ERR_TIMEOUT, where);
+  for (int i = 0; i < ring.stages; ++i) ring.wait(i, i < slot ? phase ^ 1u : phase);
+}
+
+// The place of a thread: T threads to a row, groups of max(T, 32) threads.
+struct Place {
+  int T, group_threads, group, groups, rows_per_tile, gl, rl;
+  bool first_warp;
+  __device__ __forceinline__ Place(int t)
+      : T(t), group_threads(t < 32 ? 32 : t), group(threadIdx.x / group_threads),
+        groups(blockDim.x / group_threads), rows_per_tile(group_threads / t), gl(threadIdx.x % t),
+        rl(threadIdx.x % group_threads / t), first_warp(threadIdx.x % group_threads < 32) {}
+};
+
+constexpr int kMaxBars = 8 * kMaxStages;
+
+// RES: 0 no residual, 1 BF16, 2 FP32.  W: lanes of a warp that share a row; V:
+// chunks of a thread, T * (V - 1) < cols / 8 <= T * V.
+template <int W, int V, int RES, int THREADS>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS)
 rmsnorm_fwd_kernel(const FwdParams p) {
-  __shared__ float slots[2][32];
-  const int T = G ? G : blockDim.x;
-  const int gl = G ? threadIdx.x % T : threadIdx.x;
-  const int per_cta = G ? kGroupThreads / T : 1;
-  const int64_t S = p.cols >> 5;
-  uint32_t amax = 0;
-  bool finite = true;
-  int flip = 0;
-  for (int64_t base = (int64_t)blockIdx.x * per_cta; base < p.rows;
-       base += (int64_t)gridDim.x * per_cta, flip ^= 1) {
-    const int64_t row = base + (G ? threadIdx.x / T : 0);
-    float s[V][8];
-    float ss = 0.0f;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float slots[2][16];
+  __shared__ __align__(8) uint64_t bars[kMaxBars];
+  constexpr int RSZ = RES == 2 ? 4 : 2;
+  const Place at(W < 32 ? W : p.T);
+  const int T = at.T;
+  const int64_t tiles = (p.rows + at.rows_per_tile - 1) / at.rows_per_tile;
+  const int64_t tile0 = (int64_t)blockIdx.x * at.groups + at.group, step = (int64_t)gridDim.x * at.groups;
+  const float inv_cols = 1.0f / (float)p.cols;
+  Ring<RES ? 2 : 1> ring;
+  ring.src[0] = {reinterpret_cast<const char*>(p.x), p.ldx * 2, p.cols * 2};
+  if constexpr (RES != 0) ring.src[1] = {static_cast<const char*>(p.res), p.ldr * RSZ, p.cols * RSZ};
+  ring.rows_per_tile = at.rows_per_tile;
+  ring.stage_bytes = at.rows_per_tile * p.cols * (2 + (RES ? RSZ : 0));
+  ring.rows = p.rows;
+  ring_start(ring, smem, bars, p.stages, at.group, at.groups, at.first_warp, tile0, step, tiles, p.cols,
+             p.w, p.w_f32);
+  const uint8_t* const data = smem + at.group * p.stages * ring.stage_bytes;
+  const int c0 = at.gl * 8, x_at = at.rl * p.cols + c0, r_at = at.rows_per_tile * p.cols * 2;
+  const float* const ws = reinterpret_cast<const float*>(smem + at.groups * p.stages * ring.stage_bytes) + c0;
+  const bool last = c0 + (V - 1) * T * 8 < p.cols;      // the last chunk exists
+  uint32_t amax = 0, phase = 0;
+  bool finite = true, failed = false;
+  int slot = 0, flip = 0;
+  // this thread's first column in the outputs' rows, a step of tiles at a time
+  int64_t row = tile0 * at.rows_per_tile + at.rl;
+  const int64_t row_step = step * at.rows_per_tile;
+  __nv_bfloat16* y = p.y + row * p.ldy + c0;
+  uint8_t* codes = p.codes + row * p.cols + c0;
+  uint8_t* scales = p.scales + row * (p.cols >> 5) + (c0 >> 5);
+  char* res_out = static_cast<char*>(p.res_out) + (row * p.ldo + c0) * RSZ;
+  const int64_t y_step = row_step * p.ldy, q_step = row_step * p.cols, o_step = row_step * p.ldo * RSZ;
+
+  auto body = [&](int64_t tile, auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    const bool row_ok = FULL || row < p.rows;
+    failed = !ring.wait(slot, phase);
+    const uint8_t* in = data + slot * ring.stage_bytes;
+    F8 s[V];
+    f32x2 sq = 0ull;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (gl + v * T) * 8;
-      const bool ok = row < p.rows && c < p.cols;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[v][i] = 0.0f;
-      if (ok) {
-        load8(p.x, row * p.ldx + c, false, s[v]);
+      s[v] = zero8();
+      if (FULL || (row_ok && (v < V - 1 || last))) {
+        s[v] = get8<false>(in, x_at + v * T * 8);
         if constexpr (RES != 0) {
-          float r[8];
-          load8(p.res, row * p.ldr + c, RES == 2, r);
+          const F8 r = get8<RES == 2>(in + r_at, x_at + v * T * 8);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s[v][i] += r[i];
-          store8(p.res_out, row * p.ldo + c, RES == 2, s[v]);
+          for (int i = 0; i < 4; ++i) s[v].p[i] = add2(s[v].p[i], r.p[i]);
         }
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += s[v][i] * s[v][i];
+      for (int i = 0; i < 4; ++i) sq = fma2(s[v].p[i], s[v].p[i], sq);
     }
-    ss = group_sum<G>(ss, slots[flip]);
-    const float rstd = rsqrtf(ss / (float)p.cols + p.eps);
-    if (p.rstd != nullptr && gl == 0 && row < p.rows) p.rstd[row] = rstd;
+    float ss = unpair(sq).x + unpair(sq).y;
+    ss = row_sum<W>(ss, slots[flip], T, at.group, failed);
+    if (failed) return;
+    // every thread has its part of the tile in registers: the slot is free
+    const int64_t next = tile + p.stages * step;
+    if (at.first_warp && next < tiles) ring.fetch(next, slot);
+    if (++slot == p.stages) { slot = 0; phase ^= 1u; }
+    const float rstd = rsqrtf(ss * inv_cols + p.eps);
+    if (p.rstd != nullptr && at.gl == 0 && row_ok) p.rstd[row] = rstd;
+    auto encode = [&] {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        finite &= encode8(s[v], codes + v * T * 8, scales + v * T / 4, FULL || (row_ok && (v < V - 1 || last)));
+    };
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (gl + v * T) * 8;
-      const bool ok = row < p.rows && c < p.cols;
-      float w[8], y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 0.0f;
-      if (ok) load8(p.w, c, p.w_f32, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) { s[v][i] *= rstd; y[i] = s[v][i] * w[i]; }
-      if (p.y != nullptr && ok) {
-        const uint4 packed = pack_bf16x8(y);
-        *reinterpret_cast<uint4*>(p.y + row * p.ldy + c) = packed;
-        amax = max(amax, amax_bits_bf16x8(packed));
-      } else if (ok) {
-        amax = max(amax, amax_bits_bf16x8(pack_bf16x8(y)));
-      }
-      if (p.codes != nullptr)
-        finite &= encode8(p.q_xhat ? s[v] : y, p.codes + row * p.cols + c, p.scales + row * S + (c >> 5), ok);
+      if (RES != 0 && (FULL || (row_ok && (v < V - 1 || last)))) put8<RES == 2>(res_out, v * T * 8, s[v]);
+      s[v] = scaled8(s[v], rstd);
     }
+    if (p.codes != nullptr && p.q_xhat) encode();
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (FULL || v < V - 1 || last) {
+        const F8 w = get8<true>(ws, v * T * 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[v].p[i] = mul2(s[v].p[i], w.p[i]);
+      }
+    if (p.codes != nullptr && !p.q_xhat) encode();
+    if (p.y != nullptr || p.y_amax != nullptr) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (FULL || (row_ok && (v < V - 1 || last))) {
+          const uint4 packed = pack_bf16x8(s[v]);
+          if (p.y != nullptr) *reinterpret_cast<uint4*>(y + v * T * 8) = packed;
+          if (p.y_amax != nullptr) amax = max(amax, amax_bits_bf16x8(packed));
+        }
+    }
+    row += row_step;
+    y += y_step;
+    codes += q_step;
+    scales += q_step >> 5;
+    res_out += o_step;
+  };
+  const bool whole = V * T * 8 == p.cols;
+  for (int64_t tile = tile0; tile < tiles && !failed; tile += step, flip ^= 1) {
+    if (whole && (tile + 1) * at.rows_per_tile <= p.rows) body(tile, std::true_type{});
+    else body(tile, std::false_type{});
   }
+  if (failed && at.first_warp) ring_give_up(ring, slot, phase, p.status, 0x4100);
   if (p.y_amax != nullptr) {
     amax = __reduce_max_sync(0xFFFFFFFFu, amax);
     if ((threadIdx.x & 31) == 0) atomicMax(reinterpret_cast<unsigned int*>(p.y_amax), amax);
@@ -138,154 +314,245 @@ rmsnorm_fwd_kernel(const FwdParams p) {
 }
 
 // SRC: 0 the stored sum in BF16, 1 in FP32, 2 the 8-bit checkpoint of xhat.
-template <int G, int V, int SRC>
-__global__ void __launch_bounds__(G ? kGroupThreads : 1024)
+// GF32: dres and dx in FP32.
+template <int W, int V, int SRC, bool GF32, int THREADS>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS)
 rmsnorm_bwd_kernel(const BwdParams p) {
-  __shared__ float slots[2][32];
-  extern __shared__ float sums[];        // lane groups: [groups][cols]
-  const int T = G ? G : blockDim.x;
-  const int gl = G ? threadIdx.x % T : threadIdx.x;
-  const int per_cta = G ? kGroupThreads / T : 1;
-  const int64_t S = p.cols >> 5;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float slots[2][16];
+  __shared__ __align__(8) uint64_t bars[kMaxBars];
+  constexpr int SSZ = SRC == 2 ? 1 : SRC == 1 ? 4 : 2, GSZ = GF32 ? 4 : 2;
+  const Place at(W < 32 ? W : p.T);
+  const int T = at.T;
+  const int64_t tiles = (p.rows + at.rows_per_tile - 1) / at.rows_per_tile;
+  const int64_t tile0 = (int64_t)blockIdx.x * at.groups + at.group, step = (int64_t)gridDim.x * at.groups;
   const float inv_cols = 1.0f / (float)p.cols;
-  float dw[V][8];
+  const bool has_dres = p.dres != nullptr;
+  Ring<3> ring;
+  ring.src[0] = {reinterpret_cast<const char*>(p.dy), p.lddy * 2, p.cols * 2};
+  if constexpr (SRC == 2) ring.src[1] = {reinterpret_cast<const char*>(p.codes), p.cols, p.cols};
+  else ring.src[1] = {static_cast<const char*>(p.s), p.lds * SSZ, p.cols * SSZ};
+  ring.src[2] = {static_cast<const char*>(p.dres), p.lddres * GSZ, has_dres ? p.cols * GSZ : 0};
+  ring.rows_per_tile = at.rows_per_tile;
+  ring.stage_bytes = at.rows_per_tile * (p.cols * (2 + SSZ) + ring.src[2].row_bytes);
+  ring.rows = p.rows;
+  ring_start(ring, smem, bars, p.stages, at.group, at.groups, at.first_warp, tile0, step, tiles, p.cols,
+             p.w, p.w_f32);
+  const uint8_t* const data = smem + at.group * p.stages * ring.stage_bytes;
+  const int c0 = at.gl * 8, x_at = at.rl * p.cols + c0;
+  const int s_at = at.rows_per_tile * p.cols * 2, r_at = at.rows_per_tile * p.cols * (2 + SSZ);
+  const float* const ws = reinterpret_cast<const float*>(smem + at.groups * p.stages * ring.stage_bytes) + c0;
+  const bool last = c0 + (V - 1) * T * 8 < p.cols;
+  F8 dw[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v)
+  for (int v = 0; v < V; ++v) dw[v] = zero8();
+  bool failed = false;
+  uint32_t phase = 0;
+  int slot = 0, flip = 0;
+  int64_t row = tile0 * at.rows_per_tile + at.rl;
+  const int64_t row_step = step * at.rows_per_tile;
+  char* dx = static_cast<char*>(p.dx) + (row * p.lddx + c0) * GSZ;
+  const int64_t dx_step = row_step * p.lddx * GSZ;
+  // rstd and the checkpoint's scales come straight from memory, a tile ahead
+  const uint8_t* scales = p.scales + ((row * p.cols + c0) >> 5);
+  const int64_t scales_step = row_step * p.cols >> 5;
+  float rstd_next = 0.0f;
+  uint32_t scale_next[V];
+  auto ahead = [&](int64_t r) {
+    const bool row_ok = r < p.rows;
+    rstd_next = row_ok ? p.rstd[r] : 0.0f;
+    if constexpr (SRC == 2) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[v][i] = 0.0f;
-  int flip = 0;
-  for (int64_t base = (int64_t)blockIdx.x * per_cta; base < p.rows;
-       base += (int64_t)gridDim.x * per_cta, flip ^= 1) {
-    const int64_t row = base + (G ? threadIdx.x / T : 0);
-    const float rstd = row < p.rows ? p.rstd[row] : 0.0f;
-    float xh[V][8], g[V][8];
+      for (int v = 0; v < V; ++v) scale_next[v] = row_ok && (v < V - 1 || last) ? scales[v * T / 4] : 0u;
+      scales += scales_step;
+    }
+  };
+  ahead(row);
+
+  auto body = [&](int64_t tile, auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    const bool row_ok = FULL || row < p.rows;
+    const float rstd = rstd_next;
+    float e[V];                            // xhat = e * what is stored
+#pragma unroll
+    for (int v = 0; v < V; ++v) e[v] = SRC == 2 ? ckpt_scale(scale_next[v]) : rstd;
+    ahead(row + row_step);
+    failed = !ring.wait(slot, phase);
+    const uint8_t* in = data + slot * ring.stage_bytes;
+    // Both passes read the row from shared memory: between them a thread holds
+    // its weight sums and little else, so that two CTAs fit an SM.
+    auto stored = [&](int v) {
+      if constexpr (SRC == 2) return e4m3x8(*reinterpret_cast<const uint2*>(in + s_at + x_at + v * T * 8));
+      else return get8<SRC == 1>(in + s_at, x_at + v * T * 8);
+    };
     float dot = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (gl + v * T) * 8;
+    for (int v = 0; v < V; ++v)
+      if (FULL || (row_ok && (v < V - 1 || last))) {
+        const F8 q = stored(v), d = get8<false>(in, x_at + v * T * 8), w = get8<true>(ws, v * T * 8);
+        const f32x2 ee = pair(e[v], e[v]);
+        f32x2 part = 0ull;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) xh[v][i] = g[v][i] = 0.0f;
-      if (row < p.rows && c < p.cols) {
-        if constexpr (SRC == 2) {
-          const uint2 q = *reinterpret_cast<const uint2*>(p.codes + row * p.cols + c);
-          const float e = ckpt_scale(p.scales[row * S + (c >> 5)]);
-          e4m3x4_to_f32(q.x, xh[v]);
-          e4m3x4_to_f32(q.y, xh[v] + 4);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) xh[v][i] *= e;
-        } else {
-          load8(p.s, row * p.lds + c, SRC == 1, xh[v]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) xh[v][i] *= rstd;
+        for (int i = 0; i < 4; ++i) {
+          const f32x2 t = mul2(mul2(q.p[i], ee), d.p[i]);      // dy * xhat
+          dw[v].p[i] = add2(dw[v].p[i], t);
+          part = fma2(t, w.p[i], part);
         }
-        float dy[8], w[8];
-        load8(p.dy, row * p.lddy + c, false, dy);
-        load8(p.w, c, p.w_f32, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          g[v][i] = dy[i] * w[i];
-          dw[v][i] += dy[i] * xh[v][i];
-          dot += g[v][i] * xh[v][i];
-        }
+        dot += unpair(part).x + unpair(part).y;
       }
+    const float k = row_sum<W>(dot, slots[flip], T, at.group, failed) * inv_cols * -rstd;
+    if (failed) return;
+    // every thread is done with the tile before this one: its slot is free
+    if (p.stages > 1 && tile != tile0) {
+      const int64_t next = tile + (p.stages - 1) * step;
+      if (at.first_warp && next < tiles) ring.fetch(next, slot == 0 ? p.stages - 1 : slot - 1);
     }
-    const float m = group_sum<G>(dot, slots[flip]) * inv_cols;
+    const f32x2 rr = pair(rstd, rstd);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (gl + v * T) * 8;
-      if (row < p.rows && c < p.cols) {
-        float o[8];
+    for (int v = 0; v < V; ++v)
+      if (FULL || (row_ok && (v < V - 1 || last))) {
+        const F8 q = stored(v), d = get8<false>(in, x_at + v * T * 8), w = get8<true>(ws, v * T * 8);
+        F8 o = scaled8(q, k * e[v]);
+        if (has_dres) {
+          const F8 r = get8<GF32>(in + r_at, x_at + v * T * 8);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = rstd * (g[v][i] - xh[v][i] * m);
-        if (p.dres != nullptr) {
-          float r[8];
-          load8(p.dres, row * p.lddres + c, p.grad_f32, r);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] += r[i];
+          for (int i = 0; i < 4; ++i) o.p[i] = add2(o.p[i], r.p[i]);
         }
-        store8(p.dx, row * p.lddx + c, p.grad_f32, o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o.p[i] = fma2(mul2(d.p[i], w.p[i]), rr, o.p[i]);
+        put8<GF32>(dx, v * T * 8, o);
       }
+    if (p.stages == 1) {
+      group_sync_or(at.group, at.group_threads, false);
+      if (at.first_warp && tile + step < tiles) ring.fetch(tile + step, 0);
     }
+    if (++slot == p.stages) { slot = 0; phase ^= 1u; }
+    row += row_step;
+    dx += dx_step;
+  };
+  const bool whole = V * T * 8 == p.cols;
+  for (int64_t tile = tile0; tile < tiles && !failed; tile += step, flip ^= 1) {
+    if (whole && (tile + 1) * at.rows_per_tile <= p.rows) body(tile, std::true_type{});
+    else body(tile, std::false_type{});
   }
+  if (failed && at.first_warp) ring_give_up(ring, slot, phase, p.status, 0x4200);
   if (p.partial == nullptr) return;
+  // join the CTA's rows through shared memory (no copies are on their way: every
+  // one that was issued has been waited for)
+  const int rows_held = at.groups * at.rows_per_tile;
   float* out = p.partial + (int64_t)blockIdx.x * p.cols;
-  if constexpr (G == 0) {
+  __syncthreads();
+  float* sums = rows_held == 1 ? out + c0
+                               : reinterpret_cast<float*>(smem) + (at.group * at.rows_per_tile + at.rl) * p.cols + c0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (gl + v * T) * 8;
-      if (c < p.cols) store8(out, c, true, dw[v]);
-    }
-  } else {
-    const int grp = threadIdx.x / T;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (gl + v * T) * 8;
-      if (c < p.cols) store8(sums + grp * p.cols, c, true, dw[v]);
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < p.cols; c += kGroupThreads) {
-      float a = 0.0f;
-      for (int k = 0; k < per_cta; ++k) a += sums[k * p.cols + c];
-      out[c] = a;
-    }
+  for (int v = 0; v < V; ++v)
+    if (v < V - 1 || last) put8<true>(sums, v * T * 8, dw[v]);
+  if (rows_held == 1) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
+    float a = 0.0f;
+    for (int i = 0; i < rows_held; ++i) a += reinterpret_cast<const float*>(smem)[i * p.cols + c];
+    out[c] = a;
   }
 }
 
-// Lanes per row (0: the CTA), chunks per thread and threads of the CTA for a row
-// of `cols`: as few lanes as hold the row in one chunk each, then more chunks.
-struct RowPlan { int lanes, chunks, threads; };
-RowPlan row_plan(int64_t cols) {
+// T threads to a row with at most four chunks of eight columns each: 8 or 16 for
+// short rows, else whole warps.  An SM gets about 512 threads (at 128 registers),
+// as two or three CTAs where the weights' copies leave each ring two stages, else
+// as one CTA.  (One stage only, for the widest rows of four bytes a value: 0.58
+// of the copy rate against 0.84.)
+struct RowPlan { int T, chunks, threads, rows_per_cta, stages, smem, per_sm; };
+RowPlan row_plan(int64_t cols, int bytes_per_value, bool row_sums) {
   const int64_t n = cols / 8;
-  if (n <= 8) return {8, 1, kGroupThreads};
-  if (n <= 16) return {16, 1, kGroupThreads};
-  if (n <= 32) return {32, 1, kGroupThreads};
-  if (n <= 64) return {32, 2, kGroupThreads};
-  if (n <= 128) return {32, 4, kGroupThreads};
-  const int chunks = n <= 512 ? 1 : n <= 1024 ? 2 : 4;
-  const int64_t t = (n + chunks - 1) / chunks;
-  return {0, chunks, (int)((t + 31) / 32 * 32)};
+  RowPlan r{8, 0, 0, 0, 0, 0, 0};
+  if (n > 32) r.T = 16;
+  if (n > 64) r.T = (int)((n + 127) / 128) * 32;
+  r.chunks = (int)((n + r.T - 1) / r.T);
+  const int group = r.T < 32 ? 32 : r.T;
+  const int64_t weights = 4 * cols;
+  // stages that fit when the SM's 228 KB (1 KB of them and the static part of
+  // each CTA taken off) are shared by per_sm CTAs of `groups` groups
+  auto fit = [&](int groups, int per_sm) {
+    const int64_t stage = (int64_t)(groups * group / r.T) * cols * bytes_per_value;
+    const int64_t s = (228 * 1024 / per_sm - 2048 - weights) / stage;
+    r.threads = groups * group;
+    r.rows_per_cta = r.threads / r.T;
+    r.per_sm = per_sm;
+    r.stages = (int)(s < 1 ? 1 : s < kMaxStages ? s : kMaxStages);
+    r.smem = (int)(r.stages * stage + weights);
+    return s;
+  };
+  const int small = group > 256 ? 1 : 256 / group;
+  int64_t stages = 0;
+  for (int per_sm = 512 / (small * group); per_sm >= 2 && stages < 2; --per_sm) stages = fit(small, per_sm);
+  for (int groups = (r.T < 32 ? 256 : 512) / group; groups >= 1 && stages < 2; --groups) stages = fit(groups, 1);
+  const int sums = row_sums ? r.threads * r.chunks * 8 * 4 : 0;     // the rows' weight sums at the end
+  if (r.smem < sums) r.smem = sums;
+  return r;
+}
+
+template <typename P>
+cudaError_t launch_rows(void (*kernel)(const P), P& p, const RowPlan& r, int grid, cudaStream_t s) {
+  p.T = r.T;
+  p.stages = r.stages;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, r.smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, r.threads, r.smem, s>>>(p);
+  count_launches(1);
+  return cudaGetLastError();
 }
 
 template <int RES>
-cudaError_t launch_fwd(const FwdParams& p, cudaStream_t s) {
-  const RowPlan r = row_plan(p.cols);
-  const int per_cta = r.lanes ? kGroupThreads / r.lanes : 1;
-  const int64_t want = (p.rows + per_cta - 1) / per_cta;
-  const int64_t slots = (int64_t)sm_count() * (2048 / r.threads);
-  const int grid = (int)(want < slots ? want : slots);
-#define FP4_NORM_FWD(G, V) rmsnorm_fwd_kernel<G, V, RES><<<grid, r.threads, 0, s>>>(p)
-  if (r.lanes == 8) FP4_NORM_FWD(8, 1);
-  else if (r.lanes == 16) FP4_NORM_FWD(16, 1);
-  else if (r.lanes == 32 && r.chunks == 1) FP4_NORM_FWD(32, 1);
-  else if (r.lanes == 32 && r.chunks == 2) FP4_NORM_FWD(32, 2);
-  else if (r.lanes == 32) FP4_NORM_FWD(32, 4);
-  else if (r.chunks == 1) FP4_NORM_FWD(0, 1);
-  else if (r.chunks == 2) FP4_NORM_FWD(0, 2);
-  else FP4_NORM_FWD(0, 4);
-#undef FP4_NORM_FWD
-  count_launches(1);
-  return cudaGetLastError();
+cudaError_t launch_fwd(FwdParams& p, cudaStream_t s) {
+  const RowPlan r = row_plan(p.cols, 2 + (RES == 2 ? 4 : RES == 1 ? 2 : 0), false);
+  const int64_t want = (p.rows + r.rows_per_cta - 1) / r.rows_per_cta;
+  const int64_t room = (int64_t)sm_count() * r.per_sm;
+  const int grid = (int)(want < room ? want : room);
+#define FP4_FWD(W, V, THREADS) return launch_rows(rmsnorm_fwd_kernel<W, V, RES, THREADS>, p, r, grid, s)
+  if (r.T == 8) {
+    if (r.chunks == 1) FP4_FWD(8, 1, 256);
+    if (r.chunks == 2) FP4_FWD(8, 2, 256);
+    if (r.chunks == 3) FP4_FWD(8, 3, 256);
+    FP4_FWD(8, 4, 256);
+  }
+  if (r.T == 16) {
+    if (r.chunks == 3) FP4_FWD(16, 3, 256);
+    FP4_FWD(16, 4, 256);
+  }
+  if (r.threads > 256) {
+    if (r.chunks == 3) FP4_FWD(32, 3, 512);
+    FP4_FWD(32, 4, 512);
+  }
+  if (r.chunks == 3) FP4_FWD(32, 3, 256);
+  FP4_FWD(32, 4, 256);
+#undef FP4_FWD
 }
 
-template <int SRC>
-cudaError_t launch_bwd(const BwdParams& p, int& grid, cudaStream_t s) {
-  const RowPlan r = row_plan(p.cols);
-  const int per_cta = r.lanes ? kGroupThreads / r.lanes : 1;
-  const int64_t want = (p.rows + per_cta - 1) / per_cta;
-  grid = (int)(want < kMaxSlices ? want : kMaxSlices);
-  const size_t smem = r.lanes && p.partial ? (size_t)per_cta * p.cols * sizeof(float) : 0;   // <= 32 KB
-#define FP4_NORM_BWD(G, V) rmsnorm_bwd_kernel<G, V, SRC><<<grid, r.threads, smem, s>>>(p)
-  if (r.lanes == 8) FP4_NORM_BWD(8, 1);
-  else if (r.lanes == 16) FP4_NORM_BWD(16, 1);
-  else if (r.lanes == 32 && r.chunks == 1) FP4_NORM_BWD(32, 1);
-  else if (r.lanes == 32 && r.chunks == 2) FP4_NORM_BWD(32, 2);
-  else if (r.lanes == 32) FP4_NORM_BWD(32, 4);
-  else if (r.chunks == 1) FP4_NORM_BWD(0, 1);
-  else if (r.chunks == 2) FP4_NORM_BWD(0, 2);
-  else FP4_NORM_BWD(0, 4);
-#undef FP4_NORM_BWD
-  count_launches(1);
-  return cudaGetLastError();
+template <int SRC, bool GF32>
+cudaError_t launch_bwd(BwdParams& p, int& grid, cudaStream_t s) {
+  const int dres = p.dres == nullptr ? 0 : GF32 ? 4 : 2;
+  const RowPlan r = row_plan(p.cols, 2 + (SRC == 2 ? 1 : SRC == 1 ? 4 : 2) + dres, p.partial != nullptr);
+  const int64_t want = (p.rows + r.rows_per_cta - 1) / r.rows_per_cta;
+  const int64_t room = kMaxSlices / 3 * r.per_sm;
+  grid = (int)(want < room ? want : room);
+#define FP4_BWD(W, V, THREADS) return launch_rows(rmsnorm_bwd_kernel<W, V, SRC, GF32, THREADS>, p, r, grid, s)
+  if (r.T == 8) {
+    if (r.chunks == 1) FP4_BWD(8, 1, 256);
+    if (r.chunks == 2) FP4_BWD(8, 2, 256);
+    if (r.chunks == 3) FP4_BWD(8, 3, 256);
+    FP4_BWD(8, 4, 256);
+  }
+  if (r.T == 16) {
+    if (r.chunks == 3) FP4_BWD(16, 3, 256);
+    FP4_BWD(16, 4, 256);
+  }
+  if (r.threads > 256) {
+    if (r.chunks == 3) FP4_BWD(32, 3, 512);
+    FP4_BWD(32, 4, 512);
+  }
+  if (r.chunks == 3) FP4_BWD(32, 3, 256);
+  FP4_BWD(32, 4, 256);
+#undef FP4_BWD
 }
 
 fp4_status check_norm(int64_t rows, int64_t cols, const void* weight, int32_t w_dtype, const void* ws,
@@ -381,10 +648,12 @@ fp4_status fqt_rmsnorm_bwd(const void* dy, int64_t lddy, const void* sum, int64_
   p.dres = dres; p.lddres = lddres; p.dx = dx; p.lddx = lddx; p.grad_f32 = grad_dtype == FP4_OUT_F32;
   p.rows = rows; p.cols = (int)cols;
   p.partial = dweight != nullptr ? colsum_partials(ws) : nullptr;
+  p.status = static_cast<uint32_t*>(ws);
   int grid = 0;
-  cudaError_t e = xhat8 != nullptr          ? launch_bwd<2>(p, grid, s)
-                  : s_dtype == FP4_OUT_F32 ? launch_bwd<1>(p, grid, s)
-                                           : launch_bwd<0>(p, grid, s);
+  const int src = xhat8 != nullptr ? 2 : s_dtype == FP4_OUT_F32 ? 1 : 0;
+  cudaError_t e = src == 2   ? (p.grad_f32 ? launch_bwd<2, true>(p, grid, s) : launch_bwd<2, false>(p, grid, s))
+                  : src == 1 ? (p.grad_f32 ? launch_bwd<1, true>(p, grid, s) : launch_bwd<1, false>(p, grid, s))
+                             : (p.grad_f32 ? launch_bwd<0, true>(p, grid, s) : launch_bwd<0, false>(p, grid, s));
   if (e == cudaSuccess && dweight != nullptr) e = launch_colsum(p.partial, grid, cols, dweight, s);
   return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }

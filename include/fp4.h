@@ -385,7 +385,7 @@ size_t fqt_colsum_workspace_bytes(int64_t rows, int64_t cols);
  * q8 needed: y BF16; q8 the 8-bit form of y (q8_of = FQT_RMS_Y) or of xhat
  * (FQT_RMS_XHAT, the checkpoint fqt_rmsnorm_bwd takes); rstd [rows] float;
  * y_amax [1] float.  The statistics and y come from the unrounded s.
- * cols <= 32768; eps > 0; s^2 must not overflow FP32. */
+ * cols <= 16384; eps > 0; s^2 must not overflow FP32. */
 fp4_status fqt_rmsnorm_fwd(const void* x_bf16, int64_t ldx, const void* residual, int64_t ldr,
                            void* res_out, int64_t ldo, int32_t res_dtype, const void* weight,
                            int32_t w_dtype, float eps, int64_t rows, int64_t cols, void* y_bf16,

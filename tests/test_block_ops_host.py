@@ -101,7 +101,7 @@ def _fwd(lib, **o):
 @pytest.mark.parametrize("o,code", [
     (dict(x=None), NULL), (dict(w=None), NULL), (dict(y=None), NULL), (dict(res=None), NULL),
     (dict(out=None), NULL), (dict(cols=60, ldx=60), SHAPE), (dict(cols=0), SHAPE),
-    (dict(cols=32776, ldx=32776), SHAPE), (dict(rows=-1), SHAPE), (dict(ldx=56), SHAPE),
+    (dict(cols=16392, ldx=16392), SHAPE), (dict(rows=-1), SHAPE), (dict(ldx=56), SHAPE),
     (dict(ldy=56), SHAPE), (dict(ldx=68), ALIGN), (dict(x=C.c_void_p((1 << 20) + 2)), ALIGN),
     (dict(w=C.c_void_p((1 << 20) + 8)), ALIGN), (dict(rt=2), FORMAT), (dict(wt=5), FORMAT),
     (dict(eps=0.0), FORMAT), (dict(eps=float("nan")), FORMAT), (dict(eps=float("inf")), FORMAT),
