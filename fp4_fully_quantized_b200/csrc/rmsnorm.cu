@@ -459,10 +459,15 @@ rmsnorm_bwd_kernel(const BwdParams p) {
 // T threads to a row with at most four chunks of eight columns each: 8 or 16 for
 // short rows, else whole warps.  An SM gets about 512 threads (at 128 registers),
 // as two or three CTAs where the weights' copies leave each ring two stages, else
-// as one CTA.  (One stage only, for the widest rows of four bytes a value: 0.58
-// of the copy rate against 0.84.)
+// as one CTA (one stage, in the backward of 8192 columns: 0.67 of the copy rate
+// against 0.85).  A forward that moves nine bytes a value or more gets 256
+// threads: fewer rows at a time are in flight then, and the memory's mix of reads
+// and writes runs better (32768x4096 with an FP32 residual and a checkpoint, 13
+// bytes: 0.95 of the copy rate against 0.86; 16384x8192, 9 bytes: 0.95 against
+// 0.84); below, 256 threads do not issue fast enough (4 bytes: 0.69 against 0.94;
+// 8 bytes: 0.86 against 0.88).
 struct RowPlan { int T, chunks, threads, rows_per_cta, stages, smem, per_sm; };
-RowPlan row_plan(int64_t cols, int bytes_per_value, bool row_sums) {
+RowPlan row_plan(int64_t cols, int bytes_per_value, bool row_sums, bool few) {
   const int64_t n = cols / 8;
   RowPlan r{8, 0, 0, 0, 0, 0, 0};
   if (n > 32) r.T = 16;
@@ -483,7 +488,7 @@ RowPlan row_plan(int64_t cols, int bytes_per_value, bool row_sums) {
     return s;
   };
   const int small = group > 256 ? 1 : 256 / group;
-  int64_t stages = 0;
+  int64_t stages = few && group <= 256 ? fit((256 + group - 1) / group, 1) : 0;
   for (int per_sm = 512 / (small * group); per_sm >= 2 && stages < 2; --per_sm) stages = fit(small, per_sm);
   for (int groups = (r.T < 32 ? 256 : 512) / group; groups >= 1 && stages < 2; --groups) stages = fit(groups, 1);
   const int sums = row_sums ? r.threads * r.chunks * 8 * 4 : 0;     // the rows' weight sums at the end
@@ -504,7 +509,8 @@ cudaError_t launch_rows(void (*kernel)(const P), P& p, const RowPlan& r, int gri
 
 template <int RES>
 cudaError_t launch_fwd(FwdParams& p, cudaStream_t s) {
-  const RowPlan r = row_plan(p.cols, 2 + (RES == 2 ? 4 : RES == 1 ? 2 : 0), false);
+  const int in = 2 + (RES == 2 ? 4 : RES == 1 ? 2 : 0), out = in - 2 + (p.y ? 2 : 0) + (p.codes ? 1 : 0);
+  const RowPlan r = row_plan(p.cols, in, false, in + out >= 9);
   const int64_t want = (p.rows + r.rows_per_cta - 1) / r.rows_per_cta;
   const int64_t room = (int64_t)sm_count() * r.per_sm;
   const int grid = (int)(want < room ? want : room);
@@ -531,7 +537,7 @@ cudaError_t launch_fwd(FwdParams& p, cudaStream_t s) {
 template <int SRC, bool GF32>
 cudaError_t launch_bwd(BwdParams& p, int& grid, cudaStream_t s) {
   const int dres = p.dres == nullptr ? 0 : GF32 ? 4 : 2;
-  const RowPlan r = row_plan(p.cols, 2 + (SRC == 2 ? 1 : SRC == 1 ? 4 : 2) + dres, p.partial != nullptr);
+  const RowPlan r = row_plan(p.cols, 2 + (SRC == 2 ? 1 : SRC == 1 ? 4 : 2) + dres, p.partial != nullptr, false);
   const int64_t want = (p.rows + r.rows_per_cta - 1) / r.rows_per_cta;
   const int64_t room = kMaxSlices / 3 * r.per_sm;
   grid = (int)(want < room ? want : room);
