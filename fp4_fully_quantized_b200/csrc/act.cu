@@ -2,15 +2,17 @@
 // input: forward (with encoding), recomputation from a checkpoint, backward
 // (with the bias gradient).
 //
-// Elementwise and bound by HBM: a thread owns eight columns (of both halves
-// when gated) and walks down its rows, so the bias gradient sums in registers
-// and needs no atomics.  A CTA has `lanes` threads side by side (8, 16 or 32: 64
-// to 256 columns) and 256 / lanes rows at a time; a grid column covers the
-// width, a grid row a slice of the rows.
+// Elementwise and bound by HBM, so the loads of two rows are issued before the
+// arithmetic of either, and the arithmetic runs on pairs (act_device.cuh).  A
+// thread owns eight columns (of both halves when gated) and walks down its rows:
+// the bias gradient sums in registers and needs no atomics.  A CTA has `lanes`
+// threads side by side (8, 16 or 32: 64 to 256 columns) and 256 / lanes rows at a
+// time; a grid column covers the width, a grid row a slice of the rows.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "act_device.cuh"
 #include "fp4_device.cuh"
@@ -33,21 +35,39 @@ struct ActParams {
   int lanes;
 };
 
-// Eight values of z at (row, c).
+// Where a thread's eight values of z are, row by row, and the values of one row
+// as they are stored.
 template <bool CKPT>
-__device__ __forceinline__ void load_z(const ActParams& p, int64_t row, int64_t c, float* v) {
-  if constexpr (CKPT) {
-    const int64_t at = row * p.zcols + c;
-    const uint2 q = *reinterpret_cast<const uint2*>(p.codes + at);
-    const float e = ckpt_scale(p.scales[at >> 5]);
-    e4m3x4_to_f32(q.x, v);
-    e4m3x4_to_f32(q.y, v + 4);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= e;
-  } else {
-    load8(p.z, row * p.ldz + c, false, v);
+struct Stored;
+template <>
+struct Stored<false> {
+  struct At {
+    const __nv_bfloat16* z; int64_t step;
+    __device__ __forceinline__ At(const ActParams& p, int64_t row, int64_t c, int64_t rows)
+        : z(p.z + row * p.ldz + c), step(rows * p.ldz) {}
+    __device__ __forceinline__ void next() { z += step; }
+  };
+  uint4 q;
+  __device__ __forceinline__ void load(const At& at) { q = ld_stream(at.z); }
+  __device__ __forceinline__ F8 values() const { return bf16x8(q); }
+};
+template <>
+struct Stored<true> {
+  struct At {
+    const uint8_t* codes; const uint8_t* scales; int64_t step;
+    __device__ __forceinline__ At(const ActParams& p, int64_t row, int64_t c, int64_t rows)
+        : codes(p.codes + row * p.zcols + c), scales(p.scales + ((row * p.zcols + c) >> 5)),
+          step(rows * p.zcols) {}
+    __device__ __forceinline__ void next() { codes += step; scales += step >> 5; }
+  };
+  uint2 q;
+  uint32_t byte;
+  __device__ __forceinline__ void load(const At& at) {
+    q = ld_stream2(at.codes);
+    byte = *at.scales;
   }
-}
+  __device__ __forceinline__ F8 values() const { return scaled8(e4m3x8(q), ckpt_scale(byte)); }
+};
 
 __device__ __forceinline__ void max_to(float* dst, uint32_t amax) {
   if (dst == nullptr) return;
@@ -55,111 +75,156 @@ __device__ __forceinline__ void max_to(float* dst, uint32_t amax) {
   if ((threadIdx.x & 31) == 0) atomicMax(reinterpret_cast<unsigned int*>(dst), amax);
 }
 
+// Rows whose loads are in flight together: about 40 KB an SM cover the memory's
+// latency, and a row of a checkpoint is half a row of BF16 (recomputing ReLU with
+// two rows: 0.77 of the copy rate).
+constexpr int kRows = 2, kCkptFwdRows = 4;
+
 template <int ACT, bool GATED, bool CKPT>
-__global__ void __launch_bounds__(kThreads) act_fwd_kernel(const ActParams p) {
+__global__ void __launch_bounds__(kThreads, 4) act_fwd_kernel(const ActParams p) {
   const int lane = threadIdx.x % p.lanes, rows_at_once = kThreads / p.lanes;
   const int64_t c = ((int64_t)blockIdx.x * p.lanes + lane) * 8;
-  const bool in = c < p.cols;
+  const int64_t step = (int64_t)gridDim.y * rows_at_once;
   uint32_t amax = 0;
   bool finite = true;
-  for (int64_t base = (int64_t)blockIdx.y * rows_at_once; base < p.rows;
-       base += (int64_t)gridDim.y * rows_at_once) {
-    const int64_t row = base + threadIdx.x / p.lanes;
-    const bool ok = in && row < p.rows;
-    float g[8], u[8];
+  if (c < p.cols) {
+    int64_t row = (int64_t)blockIdx.y * rows_at_once + threadIdx.x / p.lanes;
+    typename Stored<CKPT>::At g_at(p, row, c, step), u_at(p, row, p.cols + c, step);
+    __nv_bfloat16* out = p.out + row * p.ldo + c;
+    uint8_t* codes = p.codes_out + row * p.zcols + c;
+    uint8_t* scales = p.scales_out + ((row * p.zcols + c) >> 5);
+    const int64_t out_step = step * p.ldo, z_step = step * p.zcols;
+    auto body = [&](auto rows) {
+      constexpr int N = decltype(rows)::value;
+      Stored<CKPT> gs[N], us[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = u[i] = 0.0f;
-    if (ok) {
-      load_z<CKPT>(p, row, c, g);
-      if constexpr (GATED) load_z<CKPT>(p, row, p.cols + c, u);
-    }
-    if (p.out != nullptr && ok) {
-      float y[8];
+      for (int k = 0; k < N; ++k) {
+        gs[k].load(g_at);
+        g_at.next();
+        if constexpr (GATED) {
+          us[k].load(u_at);
+          u_at.next();
+        }
+      }
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        y[i] = g[i];
-        y[i + 1] = g[i + 1];
-        act_value2<ACT>(y[i], y[i + 1]);
-        if constexpr (GATED) { y[i] *= u[i]; y[i + 1] *= u[i + 1]; }
+      for (int k = 0; k < N; ++k) {
+        const F8 g = gs[k].values();
+        F8 u;
+        if constexpr (GATED) u = us[k].values();
+        if constexpr (!CKPT) {
+          if (p.codes_out != nullptr) {
+            finite &= encode8(g, codes, scales, true);
+            if constexpr (GATED) finite &= encode8(u, codes + p.cols, scales + (p.cols >> 5), true);
+            codes += z_step;
+            scales += z_step >> 5;
+          }
+        }
+        if (p.out != nullptr) {
+          F8 y;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y.p[i] = act_value2<ACT>(g.p[i]);
+            if constexpr (GATED) y.p[i] = mul2(y.p[i], u.p[i]);
+          }
+          const uint4 packed = pack_bf16x8(y);
+          *reinterpret_cast<uint4*>(out) = packed;
+          out += out_step;
+          if (p.amax != nullptr) amax = max(amax, amax_bits_bf16x8(packed));
+        }
       }
-      const uint4 packed = pack_bf16x8(y);
-      *reinterpret_cast<uint4*>(p.out + row * p.ldo + c) = packed;
-      amax = max(amax, amax_bits_bf16x8(packed));
-    }
-    if constexpr (!CKPT) {
-      if (p.codes_out != nullptr) {
-        const int64_t at = row * p.zcols + c;
-        finite &= encode8(g, p.codes_out + at, p.scales_out + (at >> 5), ok);
-        if constexpr (GATED)
-          finite &= encode8(u, p.codes_out + at + p.cols, p.scales_out + ((at + p.cols) >> 5), ok);
-      }
-    }
+    };
+    constexpr int R = CKPT ? kCkptFwdRows : kRows;
+    for (; row + (R - 1) * step < p.rows; row += R * step) body(std::integral_constant<int, R>{});
+    for (; row < p.rows; row += step) body(std::integral_constant<int, 1>{});
   }
+  __syncwarp();
   max_to(p.amax, amax);
   if (!finite) set_status(p.status, FP4_ERR_NONFINITE, 7);
 }
 
-template <int ACT, bool GATED, bool CKPT>
-__global__ void __launch_bounds__(kThreads) act_bwd_kernel(const ActParams p) {
-  __shared__ float sums[kThreads * 8];
+template <int ACT, bool GATED, bool CKPT, bool DBIAS>
+__global__ void __launch_bounds__(kThreads, GATED && DBIAS ? 3 : 4) act_bwd_kernel(const ActParams p) {
   const int lane = threadIdx.x % p.lanes, rows_at_once = kThreads / p.lanes;
   const int64_t c = ((int64_t)blockIdx.x * p.lanes + lane) * 8;
-  const bool in = c < p.cols;
+  const int64_t step = (int64_t)gridDim.y * rows_at_once;
   uint32_t amax = 0;
-  float db[GATED ? 16 : 8];
+  F8 db = zero8(), dbu = zero8();
+  if (c < p.cols) {
+    int64_t row = (int64_t)blockIdx.y * rows_at_once + threadIdx.x / p.lanes;
+    typename Stored<CKPT>::At g_at(p, row, c, step), u_at(p, row, p.cols + c, step);
+    const __nv_bfloat16* dy_at = p.dy + row * p.lddy + c;
+    __nv_bfloat16* out = p.out + row * p.ldo + c;
+    const int64_t dy_step = step * p.lddy, out_step = step * p.ldo;
+    auto body = [&](auto rows) {
+      constexpr int N = decltype(rows)::value;
+      Stored<CKPT> gs[N], us[N];
+      uint4 dys[N];
 #pragma unroll
-  for (int i = 0; i < (GATED ? 16 : 8); ++i) db[i] = 0.0f;
-  for (int64_t row = (int64_t)blockIdx.y * rows_at_once + threadIdx.x / p.lanes; in && row < p.rows;
-       row += (int64_t)gridDim.y * rows_at_once) {
-    float g[8], dy[8], d[8];
-    load_z<CKPT>(p, row, c, g);
-    load8(p.dy, row * p.lddy + c, false, dy);
-    if constexpr (GATED) {
-      float u[8], du[8];
-      load_z<CKPT>(p, row, p.cols + c, u);
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        float f[2], df[2];
-        act_both2<ACT>(g[i], g[i + 1], f[0], f[1], df[0], df[1]);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          d[i + j] = dy[i + j] * u[i + j] * df[j];
-          du[i + j] = dy[i + j] * f[j];
-          db[8 + i + j] += du[i + j];
+      for (int k = 0; k < N; ++k) {
+        gs[k].load(g_at);
+        g_at.next();
+        if constexpr (GATED) {
+          us[k].load(u_at);
+          u_at.next();
         }
+        dys[k] = ld_stream(dy_at);
+        dy_at += dy_step;
       }
-      const uint4 packed = pack_bf16x8(du);
-      *reinterpret_cast<uint4*>(p.out + row * p.ldo + p.cols + c) = packed;
-      amax = max(amax, amax_bits_bf16x8(packed));
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        float f[2], df[2];
-        act_both2<ACT>(g[i], g[i + 1], f[0], f[1], df[0], df[1]);
-        d[i] = dy[i] * df[0];
-        d[i + 1] = dy[i + 1] * df[1];
+      for (int k = 0; k < N; ++k) {
+        const F8 g = gs[k].values(), dy = bf16x8(dys[k]);
+        F8 d;
+        if constexpr (GATED) {
+          const F8 u = us[k].values();
+          F8 du;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f32x2 f, df;
+            act_both2<ACT>(g.p[i], f, df);
+            d.p[i] = mul2(mul2(dy.p[i], u.p[i]), df);
+            du.p[i] = mul2(dy.p[i], f);
+            if constexpr (DBIAS) dbu.p[i] = add2(dbu.p[i], du.p[i]);
+          }
+          const uint4 packed = pack_bf16x8(du);
+          *reinterpret_cast<uint4*>(out + p.cols) = packed;
+          if (p.amax != nullptr) amax = max(amax, amax_bits_bf16x8(packed));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f32x2 f, df;
+            act_both2<ACT>(g.p[i], f, df);
+            d.p[i] = mul2(dy.p[i], df);
+          }
+        }
+        if constexpr (DBIAS)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) db.p[i] = add2(db.p[i], d.p[i]);
+        const uint4 packed = pack_bf16x8(d);
+        *reinterpret_cast<uint4*>(out) = packed;
+        out += out_step;
+        if (p.amax != nullptr) amax = max(amax, amax_bits_bf16x8(packed));
       }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) db[i] += d[i];
-    const uint4 packed = pack_bf16x8(d);
-    *reinterpret_cast<uint4*>(p.out + row * p.ldo + c) = packed;
-    amax = max(amax, amax_bits_bf16x8(packed));
+    };
+    for (; row + (kRows - 1) * step < p.rows; row += kRows * step) body(std::integral_constant<int, kRows>{});
+    for (; row < p.rows; row += step) body(std::integral_constant<int, 1>{});
   }
+  __syncwarp();
   max_to(p.amax, amax);
-  if (p.partial == nullptr) return;
-  // join the CTA's rows, half by half
-  const int width = p.lanes * 8;
+  if constexpr (DBIAS) {
+    // join the CTA's rows, half by half
+    __shared__ float sums[kThreads * 8];
+    const int width = p.lanes * 8;
 #pragma unroll
-  for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-    __syncthreads();
-    store8(sums, threadIdx.x * 8, true, db + 8 * h);
-    __syncthreads();
-    const int64_t col = (int64_t)blockIdx.x * width + threadIdx.x;
-    if (threadIdx.x < width && col < p.cols) {
-      float a = 0.0f;
-      for (int k = 0; k < rows_at_once; ++k) a += sums[k * width + threadIdx.x];
-      p.partial[(int64_t)blockIdx.y * p.zcols + h * p.cols + col] = a;
+    for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+      __syncthreads();
+      put8<true>(sums, threadIdx.x * 8, h == 0 ? db : dbu);
+      __syncthreads();
+      const int64_t col = (int64_t)blockIdx.x * width + threadIdx.x;
+      if (threadIdx.x < width && col < p.cols) {
+        float a = 0.0f;
+        for (int k = 0; k < rows_at_once; ++k) a += sums[k * width + threadIdx.x];
+        p.partial[(int64_t)blockIdx.y * p.zcols + h * p.cols + col] = a;
+      }
     }
   }
 }
@@ -167,22 +232,32 @@ __global__ void __launch_bounds__(kThreads) act_bwd_kernel(const ActParams p) {
 // Lanes side by side: as few of 8, 16, 32 as cover the width in one CTA.
 int lanes_for(int64_t cols) { return cols <= 64 ? 8 : cols <= 128 ? 16 : 32; }
 
-// Row slices of the grid: enough CTAs for every SM to hold eight, at most one
-// per group of rows, at most kMaxSlices (the partial sums' bound).  The size of
-// the part is a constant here, so that sums do not depend on the device.
-dim3 act_grid(int64_t rows, int64_t cols, int lanes) {
+// Row slices of the grid, for a part of 148 SMs with `per_sm` CTAs each at a time:
+// among up to 64 slices (and no more than there are groups of rows) the
+// one whose last wave is fullest, the fewest of those.  148 is a constant here,
+// so that sums do not depend on the device.
+dim3 act_grid(int64_t rows, int64_t cols, int lanes, int per_sm) {
+  const int64_t wave = 148 * per_sm;
   const int64_t gx = (cols + lanes * 8 - 1) / (lanes * 8);
-  const int64_t most = (rows + kThreads / lanes - 1) / (kThreads / lanes);
-  int64_t gy = (148 * 8 + gx - 1) / gx;
-  gy = gy < most ? gy : most;
-  gy = gy < kMaxSlices ? gy : kMaxSlices;
-  return dim3((unsigned)gx, (unsigned)gy);
+  const int64_t groups = (rows + kThreads / lanes - 1) / (kThreads / lanes);
+  const int64_t least = gx >= wave ? 1 : wave / gx;              // one wave at least
+  const int64_t most = least > 64 ? least : 64;
+  int64_t best = 1;
+  double full = -1.0;
+  for (int64_t gy = least; gy <= most && gy <= groups && gy <= kMaxSlices; ++gy) {
+    const int64_t n = gx * gy, waves = (n + wave - 1) / wave;
+    const double f = (double)n / (double)(waves * wave);
+    if (f > full + 0.01) { full = f; best = gy; }
+  }
+  if (full < 0.0) best = groups < kMaxSlices ? groups : kMaxSlices;   // fewer groups than a wave
+  return dim3((unsigned)gx, (unsigned)best);
 }
 
 template <bool FWD, int ACT, bool GATED, bool CKPT>
 void launch_one(const ActParams& p, dim3 grid, cudaStream_t s) {
   if constexpr (FWD) act_fwd_kernel<ACT, GATED, CKPT><<<grid, kThreads, 0, s>>>(p);
-  else act_bwd_kernel<ACT, GATED, CKPT><<<grid, kThreads, 0, s>>>(p);
+  else if (p.partial != nullptr) act_bwd_kernel<ACT, GATED, CKPT, true><<<grid, kThreads, 0, s>>>(p);
+  else act_bwd_kernel<ACT, GATED, CKPT, false><<<grid, kThreads, 0, s>>>(p);
 }
 
 template <bool FWD, int ACT>
@@ -196,7 +271,7 @@ void launch_act(const ActParams& p, bool gated, bool ckpt, dim3 grid, cudaStream
 template <bool FWD>
 cudaError_t launch(ActParams& p, int act, bool gated, unsigned& slices, cudaStream_t s) {
   p.lanes = lanes_for(p.cols);
-  const dim3 grid = act_grid(p.rows, p.cols, p.lanes);
+  const dim3 grid = act_grid(p.rows, p.cols, p.lanes, !FWD && gated && p.partial != nullptr ? 3 : 4);
   slices = grid.y;
   switch (act) {
     case FQT_ACT_RELU: launch_act<FWD, FQT_ACT_RELU>(p, gated, p.codes != nullptr, grid, s); break;

@@ -69,9 +69,43 @@ __device__ __forceinline__ float max_abs3(float m, float a, float b) {
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
 // ---------------------------------------------------------------------------
-// Activations.  silu(z) = z p, p = 1 / (1 + exp(-z)); gelu(z) = z Phi(z) with
-// the normal CDF Phi; gelu_tanh(z) = z (1 + tanh u) / 2 = z p(2u),
-// u = sqrt(2/pi) (z + 0.044715 z^3).  Exponential and reciprocal are the
+// Eight consecutive FP32 values as four pairs: one instruction multiplies or adds
+// two of them (fma.rn.f32x2), each rounded as the scalar form rounds it.  The
+// kernels that use this are bound by instruction issue where they are not bound
+// by HBM.
+// ---------------------------------------------------------------------------
+typedef unsigned long long f32x2;
+struct F8 { f32x2 p[4]; };
+
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// ---------------------------------------------------------------------------
+// Activations, two values at a time.  silu(z) = z p, p = 1 / (1 + exp(-z));
+// gelu(z) = z Phi(z) with the normal CDF Phi; gelu_tanh(z) = z (1 + tanh u) / 2 =
+// z p(2u), u = sqrt(2/pi) (z + 0.044715 z^3).  Exponential and reciprocal are the
 // hardware's approximations (2 and 1 units in the last place, subnormals
 // flushed), against 2^-9 of a BF16 result.  z^2 is capped in gelu_tanh where p
 // is 0 or 1 in binary32 anyway, so that a large z does not meet Inf * 0.
@@ -86,96 +120,101 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ float logistic(float z) { return rcp_approx(1.0f + ex2_approx(-kLog2e * z)); }
-
-// The upper normal tail Q(a) = 1 - Phi(a) and e = exp(-a^2/2) at a = min(|z|, 14)
-// for two values, by the rational approximation of erfc of Abramowitz and
-// Stegun, Handbook of Mathematical Functions, 7.1.26: for x >= 0
-// erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), to
-// 1.5e-7, with x = a / sqrt(2): the exponential is the density's too.  An error
-// of 0.75e-7 is one and a quarter units of FP32's last place at 1.  Both
-// reciprocals come from one (of the product: at most 18), because the special
-// functions' pipe, a quarter as wide as the FMA's, would be the bound.
-__device__ __forceinline__ void normal_tail2(float z0, float z1, float& a0, float& a1, float& q0,
-                                             float& q1, float& e0, float& e1) {
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(a0) : "f"(fabsf(z0)), "f"(14.0f));
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(a1) : "f"(fabsf(z1)), "f"(14.0f));
-  const float d0 = 1.0f + 0.23164190f * a0, d1 = 1.0f + 0.23164190f * a1;   // 0.3275911 / sqrt(2)
-  const float r = rcp_approx(d0 * d1);
-  const float t0 = r * d1, t1 = r * d0;
-  e0 = ex2_approx((-0.5f * kLog2e) * a0 * a0);
-  e1 = ex2_approx((-0.5f * kLog2e) * a1 * a1);
-  const auto poly = [](float t) {            // half of a1 t + ... + a5 t^5
-    float q = 0.5f * 1.061405429f;
-    q = q * t - 0.5f * 1.453152027f;
-    q = q * t + 0.5f * 1.421413741f;
-    q = q * t - 0.5f * 0.284496736f;
-    q = q * t + 0.5f * 0.254829592f;
-    return q * t;
-  };
-  q0 = poly(t0) * e0;
-  q1 = poly(t1) * e1;
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 both(float v) { return pair(v, v); }
 
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTwoC = 1.5957691216057308f;          // 2 sqrt(2/pi)
 
-template <int ACT>
-__device__ __forceinline__ void act_both(float z, float& f, float& df);
+// 1 / (1 + 2^t)
+__device__ __forceinline__ f32x2 logistic2(f32x2 t) {
+  const float2 x = unpair(t);
+  const float2 d = unpair(add2(pair(ex2_approx(x.x), ex2_approx(x.y)), both(1.0f)));
+  return pair(rcp_approx(d.x), rcp_approx(d.y));
+}
 
-// The values at z0 and z1, in place.
+// The upper normal tail Q(a) = 1 - Phi(a) and e = exp(-a^2/2) at a = min(|z|, 14),
+// by the rational approximation of erfc of Abramowitz and Stegun, Handbook of
+// Mathematical Functions, 7.1.26: for x >= 0 erfc(x) = (a1 t + ... + a5 t^5) *
+// exp(-x^2), t = 1 / (1 + 0.3275911 x), to 1.5e-7, with x = a / sqrt(2): the
+// exponential is the density's too.  An error of 0.75e-7 is one and a quarter
+// units of FP32's last place at 1.  Both reciprocals come from one (of the
+// product: at most 18), because the special functions' pipe, a quarter as wide
+// as the FMA's, would be the bound.
+__device__ __forceinline__ void normal_tail2(float2 z, f32x2& a, f32x2& q, f32x2& e) {
+  a = pair(min_nan(fabsf(z.x), 14.0f), min_nan(fabsf(z.y), 14.0f));
+  const float2 d = unpair(fma2(a, both(0.23164190f), both(1.0f)));      // 0.3275911 / sqrt(2)
+  const float r = rcp_approx(d.x * d.y);
+  const f32x2 t = mul2(both(r), pair(d.y, d.x));
+  const float2 x = unpair(mul2(mul2(a, both(-0.5f * kLog2e)), a));
+  e = pair(ex2_approx(x.x), ex2_approx(x.y));
+  q = fma2(t, both(0.5f * 1.061405429f), both(-0.5f * 1.453152027f));
+  q = fma2(q, t, both(0.5f * 1.421413741f));
+  q = fma2(q, t, both(-0.5f * 0.284496736f));
+  q = fma2(q, t, both(0.5f * 0.254829592f));
+  q = mul2(mul2(q, t), e);
+}
+
+// act(z)
 template <int ACT>
-__device__ __forceinline__ void act_value2(float& z0, float& z1) {
+__device__ __forceinline__ f32x2 act_value2(f32x2 z) {
+  if constexpr (ACT == FQT_ACT_NONE) return z;
+  const float2 v = unpair(z);
+  if constexpr (ACT == FQT_ACT_RELU) return pair(max_nan(v.x, 0.0f), max_nan(v.y, 0.0f));
+  if constexpr (ACT == FQT_ACT_SILU) return mul2(z, logistic2(mul2(z, both(-kLog2e))));
   if constexpr (ACT == FQT_ACT_GELU) {
     // z Phi(z) = max(z, 0) - |z| Q(|z|)
-    float a0, a1, q0, q1, e0, e1;
-    normal_tail2(z0, z1, a0, a1, q0, q1, e0, e1);
-    z0 = fmaxf(z0, 0.0f) - a0 * q0;
-    z1 = fmaxf(z1, 0.0f) - a1 * q1;
-  } else {
-    float d;
-    act_both<ACT>(z0, z0, d);
-    act_both<ACT>(z1, z1, d);
-  }
-}
-
-// The value and the derivative at z (not GELU).
-template <int ACT>
-__device__ __forceinline__ void act_both(float z, float& f, float& df) {
-  static_assert(ACT != FQT_ACT_GELU, "in pairs: act_both2");
-  if constexpr (ACT == FQT_ACT_NONE) { f = z; df = 1.0f; }
-  if constexpr (ACT == FQT_ACT_RELU) {
-    f = z > 0.0f ? z : (z != z ? z : 0.0f);
-    df = z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
-  }
-  if constexpr (ACT == FQT_ACT_SILU) {
-    const float p = logistic(z);
-    f = z * p;
-    df = p + f * (1.0f - p);
+    f32x2 a, q, e;
+    normal_tail2(v, a, q, e);
+    return fma2(mul2(a, both(-1.0f)), q, pair(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
   }
   if constexpr (ACT == FQT_ACT_GELU_TANH) {
-    const float z2 = fminf(z * z, 1e4f);
-    const float p = logistic(kTwoC * z * (1.0f + 0.044715f * z2));
-    f = z * p;
-    df = p + f * (1.0f - p) * (kTwoC * (1.0f + 0.134145f * z2));
+    const float2 s = unpair(mul2(z, z));
+    const f32x2 z2 = pair(fminf(s.x, 1e4f), fminf(s.y, 1e4f));
+    return mul2(z, logistic2(mul2(z, fma2(z2, both(-kTwoC * kLog2e * 0.044715f), both(-kTwoC * kLog2e)))));
   }
 }
 
-// Values and derivatives at z0 and z1.
+// act(z) and act'(z)
 template <int ACT>
-__device__ __forceinline__ void act_both2(float z0, float z1, float& f0, float& f1, float& df0,
-                                          float& df1) {
+__device__ __forceinline__ void act_both2(f32x2 z, f32x2& f, f32x2& df) {
+  const float2 v = unpair(z);
+  if constexpr (ACT == FQT_ACT_NONE) { f = z; df = both(1.0f); }
+  if constexpr (ACT == FQT_ACT_RELU) {
+    f = act_value2<ACT>(z);
+    df = pair(v.x > 0.0f ? 1.0f : (v.x != v.x ? v.x : 0.0f), v.y > 0.0f ? 1.0f : (v.y != v.y ? v.y : 0.0f));
+  }
+  if constexpr (ACT == FQT_ACT_SILU) {
+    const f32x2 p = logistic2(mul2(z, both(-kLog2e)));
+    f = mul2(z, p);
+    df = fma2(f, fma2(p, both(-1.0f), both(1.0f)), p);
+  }
   if constexpr (ACT == FQT_ACT_GELU) {
-    // Phi + z phi: beyond |z| = 14 the second term is below 2^-126
-    float a0, a1, q0, q1, e0, e1;
-    normal_tail2(z0, z1, a0, a1, q0, q1, e0, e1);
-    f0 = fmaxf(z0, 0.0f) - a0 * q0;
-    f1 = fmaxf(z1, 0.0f) - a1 * q1;
-    df0 = (z0 < 0.0f ? q0 : 1.0f - q0) + copysignf(a0, z0) * (0.3989422804014327f * e0);
-    df1 = (z1 < 0.0f ? q1 : 1.0f - q1) + copysignf(a1, z1) * (0.3989422804014327f * e1);
-  } else {
-    act_both<ACT>(z0, f0, df0);
-    act_both<ACT>(z1, f1, df1);
+    // Phi + z phi = 1/2 +- (1/2 - Q) + z phi: beyond |z| = 14 the last is below 2^-126
+    f32x2 a, q, e;
+    normal_tail2(v, a, q, e);
+    f = fma2(mul2(a, both(-1.0f)), q, pair(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
+    const f32x2 odd = fma2(mul2(a, both(0.3989422804014327f)), e, fma2(q, both(-1.0f), both(0.5f)));
+    const float2 o = unpair(odd);
+    df = add2(pair(copysignf(o.x, v.x), copysignf(o.y, v.y)), both(0.5f));
+  }
+  if constexpr (ACT == FQT_ACT_GELU_TANH) {
+    const float2 s = unpair(mul2(z, z));
+    const f32x2 z2 = pair(fminf(s.x, 1e4f), fminf(s.y, 1e4f));
+    const f32x2 p =
+        logistic2(mul2(z, fma2(z2, both(-kTwoC * kLog2e * 0.044715f), both(-kTwoC * kLog2e))));
+    f = mul2(z, p);
+    const f32x2 slope = fma2(z2, both(kTwoC * 0.134145f), both(kTwoC));
+    df = fma2(mul2(f, fma2(p, both(-1.0f), both(1.0f))), slope, p);
   }
 }
 
@@ -235,58 +274,6 @@ __device__ __forceinline__ void store8(void* base, int64_t i, bool f32, const fl
   }
 }
 
-// A thread's eight values of a 32-column block (four neighbouring lanes hold it;
-// every lane of the warp calls this) to E4M3; false for a block with Inf or NaN.
-__device__ __forceinline__ bool encode8(const float* v, uint8_t* codes, uint8_t* scale, bool valid) {
-  uint32_t m = abs_bits(max_abs3(max_abs3(max_abs3(max_abs3(0.0f, v[0], v[1]), v[2], v[3]), v[4], v[5]),
-                                 v[6], v[7]));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-  const uint32_t byte = ckpt_scale_byte(m);
-  const float inv = ckpt_inv_scale(byte);
-  if (valid) {
-    *reinterpret_cast<uint2*>(codes) =
-        make_uint2(e4m3x4_rn(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                   e4m3x4_rn(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
-    if ((threadIdx.x & 3) == 0) *scale = (uint8_t)byte;
-  }
-  return byte != kCkptNanScale;
-}
-
-// ---------------------------------------------------------------------------
-// Eight consecutive FP32 values as four pairs: one instruction multiplies or adds
-// two of them (fma.rn.f32x2), each rounded as the scalar form rounds it.  The
-// kernels that use this are bound by instruction issue where they are not bound
-// by HBM.
-// ---------------------------------------------------------------------------
-typedef unsigned long long f32x2;
-struct F8 { f32x2 p[4]; };
-
-__device__ __forceinline__ f32x2 pair(float lo, float hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(f32x2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ F8 zero8() { return F8{{0ull, 0ull, 0ull, 0ull}}; }
 __device__ __forceinline__ F8 scaled8(const F8& v, float k) {
   const f32x2 kk = pair(k, k);
@@ -345,13 +332,14 @@ __device__ __forceinline__ void put8(void* base, int64_t i, const F8& v) {
   }
 }
 
-// A thread's eight values of a 32-column block (four neighbouring lanes hold it;
-// every lane of the warp calls this) to E4M3; false for a block with Inf or NaN.
+// A thread's eight values of a 32-column block (four neighbouring lanes hold it
+// and call this together) to E4M3; false for a block with Inf or NaN.
 __device__ __forceinline__ bool encode8(const F8& x, uint8_t* codes, uint8_t* scale, bool valid) {
   const float2 a = unpair(x.p[0]), b = unpair(x.p[1]), c = unpair(x.p[2]), d = unpair(x.p[3]);
   uint32_t m = abs_bits(max_abs3(max_abs3(max_abs3(max_abs3(0.0f, a.x, a.y), b.x, b.y), c.x, c.y), d.x, d.y));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  const uint32_t quad = 0xFu << (threadIdx.x & 28);
+  m = max(m, __shfl_xor_sync(quad, m, 1));
+  m = max(m, __shfl_xor_sync(quad, m, 2));
   const uint32_t byte = ckpt_scale_byte(m);
   if (valid) {
     const F8 v = scaled8(x, ckpt_inv_scale(byte));

@@ -106,7 +106,11 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 template <int ACT>
 __device__ __forceinline__ void act32(float* v) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) fp4dev::act_value2<ACT>(v[i], v[i + 1]);
+  for (int i = 0; i < 32; i += 2) {
+    const float2 f = fp4dev::unpair(fp4dev::act_value2<ACT>(fp4dev::pair(v[i], v[i + 1])));
+    v[i] = f.x;
+    v[i + 1] = f.y;
+  }
 }
 
 // 64 bytes of a residual row from column `col`: 32 BF16 or 16 FP32 values.
