@@ -69,12 +69,6 @@ struct Stored<true> {
   __device__ __forceinline__ F8 values() const { return scaled8(e4m3x8(q), ckpt_scale(byte)); }
 };
 
-__device__ __forceinline__ void max_to(float* dst, uint32_t amax) {
-  if (dst == nullptr) return;
-  amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-  if ((threadIdx.x & 31) == 0) atomicMax(reinterpret_cast<unsigned int*>(dst), amax);
-}
-
 // Rows whose loads are in flight together: about 40 KB an SM cover the memory's
 // latency, and a row of a checkpoint is half a row of BF16 (recomputing ReLU with
 // two rows: 0.77 of the copy rate).
@@ -85,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 4) act_fwd_kernel(const ActParams p)
   const int lane = threadIdx.x % p.lanes, rows_at_once = kThreads / p.lanes;
   const int64_t c = ((int64_t)blockIdx.x * p.lanes + lane) * 8;
   const int64_t step = (int64_t)gridDim.y * rows_at_once;
-  uint32_t amax = 0;
+  AmaxBf16 amax;
   bool finite = true;
   if (c < p.cols) {
     int64_t row = (int64_t)blockIdx.y * rows_at_once + threadIdx.x / p.lanes;
@@ -129,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 4) act_fwd_kernel(const ActParams p)
           const uint4 packed = pack_bf16x8(y);
           *reinterpret_cast<uint4*>(out) = packed;
           out += out_step;
-          if (p.amax != nullptr) amax = max(amax, amax_bits_bf16x8(packed));
+          if (p.amax != nullptr) amax.add(packed);
         }
       }
     };
@@ -138,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 4) act_fwd_kernel(const ActParams p)
     for (; row < p.rows; row += step) body(std::integral_constant<int, 1>{});
   }
   __syncwarp();
-  max_to(p.amax, amax);
+  amax.to(p.amax);
   if (!finite) set_status(p.status, FP4_ERR_NONFINITE, 7);
 }
 
@@ -147,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, GATED && DBIAS ? 3 : 4) act_bwd_kern
   const int lane = threadIdx.x % p.lanes, rows_at_once = kThreads / p.lanes;
   const int64_t c = ((int64_t)blockIdx.x * p.lanes + lane) * 8;
   const int64_t step = (int64_t)gridDim.y * rows_at_once;
-  uint32_t amax = 0;
+  AmaxBf16 amax;
   F8 db = zero8(), dbu = zero8();
   if (c < p.cols) {
     int64_t row = (int64_t)blockIdx.y * rows_at_once + threadIdx.x / p.lanes;
@@ -187,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, GATED && DBIAS ? 3 : 4) act_bwd_kern
           }
           const uint4 packed = pack_bf16x8(du);
           *reinterpret_cast<uint4*>(out + p.cols) = packed;
-          if (p.amax != nullptr) amax = max(amax, amax_bits_bf16x8(packed));
+          if (p.amax != nullptr) amax.add(packed);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -202,14 +196,14 @@ __global__ void __launch_bounds__(kThreads, GATED && DBIAS ? 3 : 4) act_bwd_kern
         const uint4 packed = pack_bf16x8(d);
         *reinterpret_cast<uint4*>(out) = packed;
         out += out_step;
-        if (p.amax != nullptr) amax = max(amax, amax_bits_bf16x8(packed));
+        if (p.amax != nullptr) amax.add(packed);
       }
     };
     for (; row + (kRows - 1) * step < p.rows; row += kRows * step) body(std::integral_constant<int, kRows>{});
     for (; row < p.rows; row += step) body(std::integral_constant<int, 1>{});
   }
   __syncwarp();
-  max_to(p.amax, amax);
+  amax.to(p.amax);
   if constexpr (DBIAS) {
     // join the CTA's rows, half by half
     __shared__ float sums[kThreads * 8];

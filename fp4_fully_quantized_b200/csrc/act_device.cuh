@@ -245,12 +245,22 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float* v) {
                     pack_bf16x2(v[6], v[7]));
 }
 
-// max |v| of eight packed BF16 values, as binary32 bits.
-__device__ __forceinline__ uint32_t amax_bits_bf16x8(const uint4& u) {
-  const uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
-                              __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
-  return max(m >> 16, m & 0xFFFFu) << 16;
-}
+// A running max |v| over packed BF16 values, two lanes; NaN stays.
+struct AmaxBf16 {
+  __nv_bfloat162 m = __nv_bfloat162(__float2bfloat16(0.0f), __float2bfloat16(0.0f));
+  __device__ __forceinline__ void add(const uint4& u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+  }
+  // into *dst (if not NULL), as binary32 bits: they order by magnitude, NaN on top
+  __device__ __forceinline__ void to(float* dst) const {
+    if (dst == nullptr) return;
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(&m);
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(w >> 16, w & 0xFFFFu) << 16);
+    if ((threadIdx.x & 31) == 0) atomicMax(reinterpret_cast<unsigned int*>(dst), top);
+  }
+};
 
 // Eight consecutive values at element i of a BF16 or FP32 array (16-byte aligned).
 __device__ __forceinline__ void load8(const void* base, int64_t i, bool f32, float* v) {

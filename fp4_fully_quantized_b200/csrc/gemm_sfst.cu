@@ -38,22 +38,31 @@ namespace fp4impl {
 namespace {
 using namespace ptx;
 
-constexpr int BM = 128, BN = 256, BK = 256, MMA_K = 64;
-constexpr int STAGES = 4;
-constexpr int A_BYTES = BM * BK / 2;          // 16 KB
-constexpr int B_BYTES = BN * BK / 2;          // 32 KB
-constexpr int SFA_BYTES = 4 * 512;
-constexpr int SFB_BYTES = 2 * 4 * 512;
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 256;
-constexpr int EPI_SMEM_BYTES = SMEM_BYTES + 8 * 128 * 4;   // and the epilogue warps' bias values
+constexpr int BM = 128, BK = 256, MMA_K = 64;
 constexpr int NUM_THREADS = 512;
 constexpr int SF_WARP0 = 0, EPI_WARP0 = 4, EPI_WARPS = 8, PRODUCER_WARP = 12, MMA_WARP = 13;
 constexpr int TMEM_COLS = 512;
-constexpr int TMEM_SF_BASE = 256;
-constexpr int TMEM_SF_STAGE = 48;             // 16 (A) + 32 (B) columns per stage
-static_assert(TMEM_SF_BASE + STAGES * TMEM_SF_STAGE <= TMEM_COLS, "TMEM budget");
-static_assert(EPI_SMEM_BYTES <= 232448, "shared-memory budget");
+
+// What depends on the tile's width BN: 256, or 128 for products of few tiles
+// (EPI kernels only, see narrow_tiles).
+template <int BN_>
+struct Tile {
+  static constexpr int BN = BN_;
+  static constexpr int STAGES = BN == 256 ? 4 : 6;
+  static constexpr int ATOM_ROWS = BN / 128;             // scale atoms of B per K block
+  static constexpr int A_BYTES = BM * BK / 2;            // 16 KB
+  static constexpr int B_BYTES = BN * BK / 2;            // 32 KB (16 KB)
+  static constexpr int SFA_BYTES = 4 * 512;
+  static constexpr int SFB_BYTES = ATOM_ROWS * 4 * 512;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 256;
+  static constexpr int EPI_SMEM_BYTES = SMEM_BYTES + EPI_WARPS * (BN / 2) * 4;   // and the bias values
+  static constexpr int TMEM_SF_BASE = BN;
+  static constexpr int TMEM_SF_STAGE = 16 + 16 * ATOM_ROWS;   // A's and B's columns per stage
+  static_assert(TMEM_SF_BASE + STAGES * TMEM_SF_STAGE <= TMEM_COLS, "TMEM budget");
+  static_assert(EPI_SMEM_BYTES <= 232448, "shared-memory budget");
+  static_assert(8 * (4 * STAGES + 3) + 8 <= 256, "barrier area");
+};
 
 struct StParams {
   const uint8_t* a_sf; const uint8_t* b_sf;
@@ -228,10 +237,15 @@ __device__ __forceinline__ void fewer_registers() {
   if constexpr (EPI) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
 }
 
-template <bool NV, bool EPI>
+template <bool NV, bool EPI, int BN>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
                      const __grid_constant__ CUtensorMap tmap_b, const StParams p) {
+  using TS = Tile<BN>;
+  constexpr int STAGES = TS::STAGES, ATOM_ROWS = TS::ATOM_ROWS;
+  constexpr int A_BYTES = TS::A_BYTES, B_BYTES = TS::B_BYTES, SFA_BYTES = TS::SFA_BYTES,
+                SFB_BYTES = TS::SFB_BYTES, STAGE_BYTES = TS::STAGE_BYTES;
+  constexpr int TMEM_SF_BASE = TS::TMEM_SF_BASE, TMEM_SF_STAGE = TS::TMEM_SF_STAGE;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -294,21 +308,25 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
         const int s = it % STAGES;
         const uint32_t ph = (it / STAGES) & 1u;
         if (!warp_wait(atoms_bar(s), ph, abort_flag, p.status, 0x3300 + s, lane)) { ok = false; break; }
-        uint32_t va[16], vb[32];
+        uint32_t va[16], vb[16 * ATOM_ROWS];
         const uint8_t* fa = sSFA(s) + lane * 16;
         const uint8_t* fb = sSFB(s) + lane * 16;
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
           const uint4 x = *reinterpret_cast<const uint4*>(fa + a * 512);
           va[4 * a] = x.x; va[4 * a + 1] = x.y; va[4 * a + 2] = x.z; va[4 * a + 3] = x.w;
+          uint32_t* const w = vb + 4 * ATOM_ROWS * a;
           const uint4 y0 = *reinterpret_cast<const uint4*>(fb + a * 512);
-          const uint4 y1 = *reinterpret_cast<const uint4*>(fb + 2048 + a * 512);
-          vb[8 * a] = y0.x; vb[8 * a + 1] = y0.y; vb[8 * a + 2] = y0.z; vb[8 * a + 3] = y0.w;
-          vb[8 * a + 4] = y1.x; vb[8 * a + 5] = y1.y; vb[8 * a + 6] = y1.z; vb[8 * a + 7] = y1.w;
+          w[0] = y0.x; w[1] = y0.y; w[2] = y0.z; w[3] = y0.w;
+          if constexpr (ATOM_ROWS == 2) {
+            const uint4 y1 = *reinterpret_cast<const uint4*>(fb + 2048 + a * 512);
+            w[4] = y1.x; w[5] = y1.y; w[6] = y1.z; w[7] = y1.w;
+          }
         }
         const uint32_t t_sfa = tmem_base + TMEM_SF_BASE + s * TMEM_SF_STAGE;
         tmem_st_x16(lane_base + t_sfa, va);
-        tmem_st_x32(lane_base + t_sfa + 16, vb);
+        if constexpr (ATOM_ROWS == 2) tmem_st_x32(lane_base + t_sfa + 16, vb);
+        else tmem_st_x16(lane_base + t_sfa + 16, vb);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
@@ -338,8 +356,8 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
     uint32_t tile_iter = 0;
     const int quad = warp & 3, half = (warp - EPI_WARP0) >> 2;
     const int c_begin = half * (BN / 2);
-    // EPI: this warp's 128 bias values, as FP32
-    float* const bias_s = reinterpret_cast<float*>(base + STAGES * STAGE_BYTES + 256) + (warp - EPI_WARP0) * 128;
+    // EPI: the bias values of this warp's columns, as FP32
+    float* const bias_s = reinterpret_cast<float*>(base + STAGES * STAGE_BYTES + 256) + (warp - EPI_WARP0) * (BN / 2);
     for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++tile_iter) {
       int mb, nb;
       tile_coords(tile, tiles_m, tiles_n, mb, nb);
@@ -351,23 +369,25 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
         // what the tile needs besides its accumulator, before the wait for that
         if (ncols > 0 && p.bias != nullptr) {
           __syncwarp();                     // the last tile's values have been read
-          float4 b;
-          const int64_t at = col + 4 * lane;
-          if (p.bias_f32) {
-            b = *reinterpret_cast<const float4*>(static_cast<const float*>(p.bias) + at);
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.bias) + at);
-            b = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u),
-                            __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xFFFF0000u));
+          if (lane < BN / 8) {
+            float4 b;
+            const int64_t at = col + 4 * lane;
+            if (p.bias_f32) {
+              b = *reinterpret_cast<const float4*>(static_cast<const float*>(p.bias) + at);
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.bias) + at);
+              b = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u),
+                              __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xFFFF0000u));
+            }
+            reinterpret_cast<float4*>(bias_s)[lane] = b;
           }
-          reinterpret_cast<float4*>(bias_s)[lane] = b;
           __syncwarp();
         }
         if (ncols > 0 && p.res != nullptr) {
           load_residual(p, row, col, res);
           // the rest of its row towards L2
           const char* src = static_cast<const char*>(p.res) + (row * p.ldr + col) * (p.res_f32 ? 4 : 2);
-          const int bytes = 128 * (p.res_f32 ? 4 : 2);
+          const int bytes = BN / 2 * (p.res_f32 ? 4 : 2);
           for (int o = 128; o < bytes; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + o));
         }
       }
@@ -375,39 +395,42 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)c_begin;
       if constexpr (EPI) {
-        // The whole row half leaves tensor memory first; then four blocks of 32
+        // The whole row half leaves tensor memory first; then blocks of 32
         // columns, two to an iteration: of one, two and four that measured
         // fastest (fewer moves of the rest than one, less code than four).
+        constexpr int COLS = BN / 2, BLOCKS = COLS / 32;
         uint32_t scales4 = 0;
-        float v[128];
+        float v[COLS];
         {
-          uint32_t r[128];
+          uint32_t r[COLS];
 #pragma unroll
-          for (int h = 0; h < 4; ++h) tmem_ld32_nowait(taddr + 32 * h, r + 32 * h);
+          for (int h = 0; h < BLOCKS; ++h) tmem_ld32_nowait(taddr + 32 * h, r + 32 * h);
           asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(acc_empty);
 #pragma unroll
-          for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
+          for (int i = 0; i < COLS; ++i) v[i] = __uint_as_float(r[i]);
         }
         if (ncols > 0) {
 #pragma unroll 1
-          for (int h = 0; h < 4; h += 2) {
+          for (int h = 0; h < BLOCKS; h += 2) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[32 * k + i] = __fmul_rn(v[32 * k + i], scale);
               scales4 |= epilogue32(p, row, col + 32 * (h + k), v + 32 * k, bias_s + 32 * (h + k), res,
-                                    h + k < 3, wide_st, amax) << (8 * (h + k));
+                                    h + k < BLOCKS - 1, wide_st, amax) << (8 * (h + k));
             }
 #pragma unroll
-            for (int i = 0; i < 64; ++i) v[i] = v[i + 64];
+            for (int i = 0; i < COLS - 64; ++i) v[i] = v[i + 64];
           }
         }
         if (p.z_codes != nullptr && ncols > 0) {
-          *reinterpret_cast<uint32_t*>(p.z_scales + ((row * p.N + col) >> 5)) = scales4;
-          // byte 255: Inf or NaN in one of the four blocks
+          uint8_t* const sc = p.z_scales + ((row * p.N + col) >> 5);
+          if constexpr (BLOCKS == 4) *reinterpret_cast<uint32_t*>(sc) = scales4;
+          else *reinterpret_cast<uint16_t*>(sc) = (uint16_t)scales4;
+          // byte 255: Inf or NaN in one of the blocks
           if (__vcmpeq4(scales4, 0xFFFFFFFFu) != 0) set_status(p.status, FP4_ERR_NONFINITE, 8);
         }
       } else if (p.out_mode == 0) {
@@ -588,7 +611,7 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
       for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x) {
         int mb, nb;
         tile_coords(tile, tiles_m, tiles_n, mb, nb);
-        const bool b_hi = (nb * 2 + 1) * 128 < p.N;
+        const bool b_hi = ATOM_ROWS == 2 && (nb * 2 + 1) * 128 < p.N;
         for (int kb = 0; kb < k_blocks; ++kb, ++it) {
           const int s = it % STAGES;
           const uint32_t ph = (it / STAGES) & 1u;
@@ -601,7 +624,7 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
           const int atom0 = kb * (NV ? 4 : 2);
           bulk_load(smem_u32(sSFA(s)), p.a_sf + ((size_t)mb * apr + atom0) * 512, atom_bytes,
                     atoms_bar(s));
-          bulk_load(smem_u32(sSFB(s)), p.b_sf + ((size_t)(2 * nb) * apr + atom0) * 512, atom_bytes,
+          bulk_load(smem_u32(sSFB(s)), p.b_sf + ((size_t)(ATOM_ROWS * nb) * apr + atom0) * 512, atom_bytes,
                     atoms_bar(s));
           if (b_hi)
             bulk_load(smem_u32(sSFB(s) + 4 * 512), p.b_sf + ((size_t)(2 * nb + 1) * apr + atom0) * 512,
@@ -642,12 +665,12 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
             uint32_t sfa_addr, sfb_addr, idesc;
             if (NV) {
               sfa_addr = t_sfa + 4 * kk;
-              sfb_addr = t_sfb + 8 * kk;
+              sfb_addr = t_sfb + 4 * ATOM_ROWS * kk;
               idesc = make_idesc(BN, BM, 0u, 0u, 0u);
             } else {
               const uint32_t byte = (uint32_t)(kk & 1) * 2u;
               sfa_addr = (t_sfa + 4 * (kk >> 1)) | (byte << 30);
-              sfb_addr = (t_sfb + 8 * (kk >> 1)) | (byte << 30);
+              sfb_addr = (t_sfb + 4 * ATOM_ROWS * (kk >> 1)) | (byte << 30);
               idesc = make_idesc(BN, BM, 1u, byte, byte);
             }
             tc_mma<NV>(tmem_base, smem_desc(a_base + kk * (MMA_K / 2), 16, 1024, 2),
@@ -716,8 +739,15 @@ bool codes_map(CUtensorMap* m, const uint8_t* codes, int64_t rows, int64_t K, ui
 
 }  // namespace
 
+// Tiles of 128 columns instead of 256 where those are at most half the SMs: twice
+// the SMs then share the K loop's operand bytes and the epilogue (128 x 4096 x
+// 4096 with bias and GELU, 16 tiles of 256 columns: 18.0 -> NNN us).  With more tiles the wide ones read fewer operand bytes a flop.
+static bool narrow_tiles(int64_t tiles_wide) { return tiles_wide * 2 <= sm_count(); }
+
 fp4_status gemm_launch(const GemmArgs& g, cudaStream_t s) {
   const bool nv = g.fmt == FP4_NVFP4;
+  const bool narrow = g.epi && narrow_tiles((g.M / BM) * ((g.N + 255) / 256));
+  const int BN = narrow ? 128 : 256;
   CUtensorMap ta, tb;
   if (!codes_map(&ta, g.a_codes, g.M, g.K, BM)) return FP4_ERR_CUDA;
   if (!codes_map(&tb, g.b_codes, g.N, g.K, BN)) return FP4_ERR_CUDA;
@@ -738,9 +768,11 @@ fp4_status gemm_launch(const GemmArgs& g, cudaStream_t s) {
   const int grid = tiles < sm_count() ? tiles : sm_count();
   if (g.c_amax != nullptr && cudaMemsetAsync(g.c_amax, 0, sizeof(float), s) != cudaSuccess)
     return FP4_ERR_CUDA;
-  const auto kernel = g.epi ? (nv ? fp4_gemm_sfst_kernel<true, true> : fp4_gemm_sfst_kernel<false, true>)
-                            : (nv ? fp4_gemm_sfst_kernel<true, false> : fp4_gemm_sfst_kernel<false, false>);
-  const int smem = g.epi ? EPI_SMEM_BYTES : SMEM_BYTES;
+  const auto kernel = narrow ? (nv ? fp4_gemm_sfst_kernel<true, true, 128> : fp4_gemm_sfst_kernel<false, true, 128>)
+                      : g.epi ? (nv ? fp4_gemm_sfst_kernel<true, true, 256> : fp4_gemm_sfst_kernel<false, true, 256>)
+                              : (nv ? fp4_gemm_sfst_kernel<true, false, 256> : fp4_gemm_sfst_kernel<false, false, 256>);
+  const int smem = narrow ? Tile<128>::EPI_SMEM_BYTES
+                   : g.epi ? Tile<256>::EPI_SMEM_BYTES : Tile<256>::SMEM_BYTES;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return FP4_ERR_CUDA;
   kernel<<<grid, NUM_THREADS, smem, s>>>(ta, tb, p);

@@ -224,7 +224,8 @@ rmsnorm_fwd_kernel(const FwdParams p) {
   const int c0 = at.gl * 8, x_at = at.rl * p.cols + c0, r_at = at.rows_per_tile * p.cols * 2;
   const float* const ws = reinterpret_cast<const float*>(smem + at.groups * p.stages * ring.stage_bytes) + c0;
   const bool last = c0 + (V - 1) * T * 8 < p.cols;      // the last chunk exists
-  uint32_t amax = 0, phase = 0;
+  AmaxBf16 amax;
+  uint32_t phase = 0;
   bool finite = true, failed = false;
   int slot = 0, flip = 0;
   // this thread's first column in the outputs' rows, a step of tiles at a time
@@ -291,7 +292,7 @@ rmsnorm_fwd_kernel(const FwdParams p) {
         if (FULL || (row_ok && (v < V - 1 || last))) {
           const uint4 packed = pack_bf16x8(s[v]);
           if (p.y != nullptr) *reinterpret_cast<uint4*>(y + v * T * 8) = packed;
-          if (p.y_amax != nullptr) amax = max(amax, amax_bits_bf16x8(packed));
+          if (p.y_amax != nullptr) amax.add(packed);
         }
     }
     row += row_step;
@@ -306,10 +307,8 @@ rmsnorm_fwd_kernel(const FwdParams p) {
     else body(tile, std::false_type{});
   }
   if (failed && at.first_warp) ring_give_up(ring, slot, phase, p.status, 0x4100);
-  if (p.y_amax != nullptr) {
-    amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-    if ((threadIdx.x & 31) == 0) atomicMax(reinterpret_cast<unsigned int*>(p.y_amax), amax);
-  }
+  __syncwarp();
+  amax.to(p.y_amax);
   if (!finite) set_status(p.status, FP4_ERR_NONFINITE, 6);
 }
 

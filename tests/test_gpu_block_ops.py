@@ -345,14 +345,15 @@ def _operands(F, m, n, k, fmt, seed=0):
     return qa, qb
 
 
-@pytest.mark.parametrize("mnk", [(128, 128, 64), (256, 384, 320), (384, 640, 256)])
+@pytest.mark.parametrize("mnk", [(128, 128, 64), (256, 384, 320), (384, 640, 1856), (1280, 2176, 192)])
 @pytest.mark.parametrize("fmt", [0, 1])
 @pytest.mark.parametrize("kind", R.ACTS)
 @pytest.mark.parametrize("out,bias,residual,ckpt", [
     ("bf16", "bf16", "bf16", True), ("f32", "f32", "f32", True), ("bf16", None, "f32", False),
     ("f32", "bf16", None, False), ("bf16", None, None, True)])
 def test_gemm_epi(gpu_lib, mnk, fmt, kind, out, bias, residual, ckpt):
-    """Against the 64-bit epilogue of the FP32 product that fp4_gemm stores."""
+    """Against the 64-bit epilogue of the FP32 product that fp4_gemm stores; the
+    last size has enough tiles for the wide ones."""
     F = gpu_lib
     m, n, k = mnk
     qa, qb = _operands(F, m, n, k, fmt)
@@ -380,22 +381,24 @@ def test_gemm_epi(gpu_lib, mnk, fmt, kind, out, bias, residual, ckpt):
     assert (cbuf[:, n:] == 7.0).all() and ws.status() == 0
 
 
-def test_gemm_epi_without_epilogue_is_the_gemm(gpu_lib):
+@pytest.mark.parametrize("m,n,k", [(256, 384, 512), (128, 4096, 4096), (1280, 2176, 320)])
+def test_gemm_epi_without_epilogue_is_the_gemm(gpu_lib, m, n, k):
     F = gpu_lib
-    qa, qb = _operands(F, 256, 384, 512, 0)
+    qa, qb = _operands(F, m, n, k, 0)
     for t in (BF16, F32):
-        a, b = torch.zeros(256, 384, dtype=t, device="cuda"), torch.zeros(256, 384, dtype=t, device="cuda")
+        a, b = torch.zeros(m, n, dtype=t, device="cuda"), torch.zeros(m, n, dtype=t, device="cuda")
         am, bm = torch.zeros(1, device="cuda"), torch.zeros(1, device="cuda")
         F.fp4_gemm(qa, qb, a, c_amax=am)
         F.fp4_gemm_epi(qa, qb, b, c_amax=bm)
         assert torch.equal(a, b) and torch.equal(am, bm)
 
 
-def test_gemm_epi_residual_in_place(gpu_lib):
+@pytest.mark.parametrize("m,n", [(256, 256), (1280, 2176)])
+def test_gemm_epi_residual_in_place(gpu_lib, m, n):
     F = gpu_lib
-    qa, qb = _operands(F, 256, 256, 256, 1)
+    qa, qb = _operands(F, m, n, 256, 1)
     for t in (BF16, F32):
-        r = rand(256, 256, seed=8, dtype=t)
+        r = rand(m, n, seed=8, dtype=t)
         c = torch.zeros_like(r)
         F.fp4_gemm_epi(qa, qb, c, act=F.ACT_SILU, residual=r)
         F.fp4_gemm_epi(qa, qb, r, act=F.ACT_SILU, residual=r)
