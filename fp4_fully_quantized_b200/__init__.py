@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from dataclasses import dataclass, field
 
 import torch
@@ -78,12 +79,6 @@ class Ckpt8C(C.Structure):
                 ("cols", C.c_int64)]
 
 
-class EpilogueC(C.Structure):
-    _fields_ = [("bias", C.c_void_p), ("residual", C.c_void_p), ("ld_residual", C.c_int64),
-                ("z8", C.POINTER(Ckpt8C)), ("act", C.c_int32), ("bias_dtype", C.c_int32),
-                ("residual_dtype", C.c_int32)]
-
-
 _lib = None
 
 
@@ -143,24 +138,16 @@ def load() -> C.CDLL:
     L.fp4_gemm_noalloc.restype = i32
     L.fp4_gemm_noalloc.argtypes = [C.POINTER(QTensorC), C.POINTER(QTensorC), C.c_float, vp, i64,
                                    i32, vp, vp]
-    f32, ck = C.c_float, C.POINTER(Ckpt8C)
     L.fqt_ckpt8_sizes.restype = None
     L.fqt_ckpt8_sizes.argtypes = [i64, i64, C.POINTER(sz), C.POINTER(sz)]
     L.fqt_colsum_workspace_bytes.restype = sz
     L.fqt_colsum_workspace_bytes.argtypes = [i64, i64]
-    L.fqt_rmsnorm_fwd.restype = i32
-    L.fqt_rmsnorm_fwd.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, i32, f32, i64, i64, vp, i64, ck,
-                                  i32, vp, vp, vp, sz, vp]
-    L.fqt_rmsnorm_bwd.restype = i32
-    L.fqt_rmsnorm_bwd.argtypes = [vp, i64, vp, i64, i32, ck, vp, vp, i32, vp, i64, vp, i64, i32, i64,
-                                  i64, vp, vp, sz, vp]
-    L.fqt_act_fwd.restype = i32
-    L.fqt_act_fwd.argtypes = [vp, i64, ck, i32, i32, i64, i64, vp, i64, ck, vp, vp, sz, vp]
-    L.fqt_act_bwd.restype = i32
-    L.fqt_act_bwd.argtypes = [vp, i64, vp, i64, ck, i32, i32, i64, i64, vp, i64, vp, vp, vp, sz, vp]
+    for f in (L.fqt_rmsnorm_fwd, L.fqt_rmsnorm_bwd, L.fqt_act_fwd, L.fqt_act_bwd):
+        f.restype = i32
+        f.argtypes = [C.c_char_p, vp, sz, vp]          # a packed argument structure, see _FWD below
     L.fp4_gemm_epi.restype = i32
-    L.fp4_gemm_epi.argtypes = [C.POINTER(QTensorC), C.POINTER(QTensorC), f32, C.POINTER(EpilogueC), vp,
-                               i64, i32, vp, vp, sz, vp]
+    L.fp4_gemm_epi.argtypes = [C.POINTER(QTensorC), C.POINTER(QTensorC), C.c_float, C.c_char_p, vp, i64,
+                               i32, vp, vp, sz, vp]
     _lib = L
     return L
 
@@ -466,6 +453,7 @@ class Ckpt8:
     codes: torch.Tensor
     scales: torch.Tensor
     _c: Ckpt8C = field(default=None, repr=False)
+    _address: int = field(default=0, repr=False)       # of _c
 
     @staticmethod
     def empty(rows: int, cols: int, device="cuda") -> "Ckpt8":
@@ -474,8 +462,8 @@ class Ckpt8:
         dev = torch.device(device)
         codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
         scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
-        return Ckpt8(rows, cols, codes, scales,
-                     Ckpt8C(codes.data_ptr(), scales.data_ptr(), rows, cols))
+        c = Ckpt8C(codes.data_ptr(), scales.data_ptr(), rows, cols)
+        return Ckpt8(rows, cols, codes, scales, c, C.addressof(c))
 
 
 _BF16, _F32 = torch.bfloat16, torch.float32
@@ -491,33 +479,45 @@ def _bad(where, name, t, want):
     raise ValueError(f"{where}: {name} must be {want}, got {got}")
 
 
+# The argument structures of include/fp4.h, packed in one go: a quarter of the
+# time of converting some twenty arguments one by one.
+_FWD = struct.Struct("@PqPqPqPPqPPPqqfiii").pack
+_BWD = struct.Struct("@PqPqPPPPqPqPqqiii").pack
+_ACT_FWD = struct.Struct("@PqPPqPPqqii").pack
+_ACT_BWD = struct.Struct("@PqPqPPqPPqqii").pack
+_EPI = struct.Struct("@PPqPiii").pack
+
+
 def _ld(where, name, t, shape, dev, f32=False):
     """Leading dimension of a row-major matrix of `shape` on device `dev`, BF16
     (or FP32 where f32)."""
-    strides = t.stride()
-    if t.shape != shape or t.get_device() != dev or strides[1] != 1 or \
-            (t.dtype is not _BF16 and not (f32 and t.dtype is _F32)):
-        _bad(where, name, t, f"a {list(shape)} row-major matrix of BF16{' or FP32' if f32 else ''} "
-                             f"on device {dev}")
-    return strides[0] if shape[0] > 1 else shape[1]
+    if t.shape == shape and t.get_device() == dev and (t.dtype is _BF16 or (f32 and t.dtype is _F32)):
+        if t.is_contiguous():
+            return shape[1]
+        strides = t.stride()
+        if strides[1] == 1:
+            return strides[0] if shape[0] > 1 else shape[1]
+    _bad(where, name, t, f"a {list(shape)} row-major matrix of BF16{' or FP32' if f32 else ''} "
+                         f"on device {dev}")
 
 
 def _vec(where, name, t, n, dev, bf16=False):
-    """Pointer of a dense FP32 (or BF16 where bf16) vector of n, None for None."""
+    """Pointer of a dense FP32 (or BF16 where bf16) vector of n, 0 for None."""
     if t is None:
-        return None
-    if t.shape != (n,) or t.get_device() != dev or (n > 1 and t.stride(0) != 1) or \
-            (t.dtype is not _F32 and not (bf16 and t.dtype is _BF16)):
-        _bad(where, name, t, f"a dense vector of {n} FP32{' or BF16' if bf16 else ''} on device {dev}")
-    return t.data_ptr()
+        return 0
+    if t.dim() == 1 and t.numel() == n and t.get_device() == dev and t.is_contiguous() and \
+            (t.dtype is _F32 or (bf16 and t.dtype is _BF16)):
+        return t.data_ptr()
+    _bad(where, name, t, f"a dense vector of {n} FP32{' or BF16' if bf16 else ''} on device {dev}")
 
 
 def _ckpt(where, name, q, rows, cols, dev):
+    """Address of a checkpoint's structure, 0 for None."""
     if q is None:
-        return None
+        return 0
     if not isinstance(q, Ckpt8) or q.rows != rows or q.cols != cols or q.codes.get_device() != dev:
         _bad(where, name, q, f"a Ckpt8 of [{rows}, {cols}] on device {dev}")
-    return C.byref(q._c)
+    return q._address
 
 
 def _work(where, ws, dev):
@@ -557,7 +557,8 @@ def fqt_rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor | Non
         _bad(me, "x", x, "a matrix")
     rows, cols = shape
     ldx = _ld(me, "x", x, shape, dev)
-    rp, ldr, op, ldo, rt, yp, ldy = None, 0, None, 0, OUT_BF16, None, 0
+    rp = ldr = op = ldo = yp = ldy = 0
+    rt = OUT_BF16
     if residual is not None and res_out is not None and residual.dtype is res_out.dtype:
         rp, ldr = residual.data_ptr(), _ld(me, "residual", residual, shape, dev, True)
         op, ldo = res_out.data_ptr(), _ld(me, "res_out", res_out, shape, dev, True)
@@ -570,9 +571,9 @@ def fqt_rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor | Non
     wsp, wsn = _work(me, ws, dev)
     h = _on_device(me, dev, stream)
     code = (_lib or load()).fqt_rmsnorm_fwd(
-        x.data_ptr(), ldx, rp, ldr, op, ldo, rt, wp, _FLOATS[weight.dtype], eps, rows, cols, yp, ldy,
-        _ckpt(me, "q8", q8, rows, cols, dev), q8_of, _vec(me, "rstd", rstd, rows, dev),
-        _vec(me, "y_amax", y_amax, 1, dev), wsp, wsn, h)
+        _FWD(x.data_ptr(), ldx, rp, ldr, op, ldo, wp, yp, ldy, _ckpt(me, "q8", q8, rows, cols, dev),
+             _vec(me, "rstd", rstd, rows, dev), _vec(me, "y_amax", y_amax, 1, dev), rows, cols, eps, rt,
+             _FLOATS[weight.dtype], q8_of), wsp, wsn, h)
     if code:
         raise Fp4Error(code, me)
 
@@ -593,7 +594,8 @@ def fqt_rmsnorm_bwd(dy: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, 
     if (s is None) == (xhat8 is None):
         raise ValueError(f"{me}: exactly one of s and xhat8")
     lddy = _ld(me, "dy", dy, shape, dev)
-    sp, lds, st, drp, lddr = None, 0, OUT_BF16, None, 0
+    sp = lds = drp = lddr = 0
+    st = OUT_BF16
     if s is not None:
         sp, lds, st = s.data_ptr(), _ld(me, "s", s, shape, dev, True), _FLOATS[s.dtype]
     lddx = _ld(me, "dx", dx, shape, dev, True)
@@ -604,13 +606,13 @@ def fqt_rmsnorm_bwd(dy: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, 
     wp = _vec(me, "weight", weight, cols, dev, True)
     dwp = _vec(me, "dweight", dweight, cols, dev)
     h = _on_device(me, dev, stream)
-    if dwp is not None and ws is None:
+    if dwp and ws is None:
         ws = Workspace.colsum(rows, cols, device=dy.device)
     wsp, wsn = _work(me, ws, dev)
     code = (_lib or load()).fqt_rmsnorm_bwd(
-        dy.data_ptr(), lddy, sp, lds, st, _ckpt(me, "xhat8", xhat8, rows, cols, dev),
-        _vec(me, "rstd", rstd, rows, dev), wp, _FLOATS[weight.dtype], drp, lddr, dx.data_ptr(), lddx,
-        _FLOATS[dx.dtype], rows, cols, dwp, wsp, wsn, h)
+        _BWD(dy.data_ptr(), lddy, sp, lds, _ckpt(me, "xhat8", xhat8, rows, cols, dev),
+             _vec(me, "rstd", rstd, rows, dev), wp, drp, lddr, dx.data_ptr(), lddx, dwp, rows, cols, st,
+             _FLOATS[weight.dtype], _FLOATS[dx.dtype]), wsp, wsn, h)
     if code:
         raise Fp4Error(code, me)
 
@@ -621,7 +623,8 @@ def fqt_act_fwd(z, y: torch.Tensor | None = None, act: int = ACT_SILU, gated: bo
     """y = act(z), or act(z[:, :F]) * z[:, F:] with gated (z [rows, 2 F]).  z is a
     BF16 matrix, or a Ckpt8 (recomputation; with ACT_NONE its decoding).  z8
     receives the 8-bit checkpoint of a matrix z (y None: encoding alone)."""
-    me, zp, ldz, zc = "fqt_act_fwd", None, 0, None
+    me = "fqt_act_fwd"
+    zp = ldz = zc = yp = ldy = 0
     src = z.codes if isinstance(z, Ckpt8) else z
     dev, zshape = src.get_device(), src.shape
     if len(zshape) != 2 or (gated and zshape[1] % 2):
@@ -632,14 +635,13 @@ def fqt_act_fwd(z, y: torch.Tensor | None = None, act: int = ACT_SILU, gated: bo
         zp, ldz = z.data_ptr(), _ld(me, "z", z, zshape, dev)
     else:
         zc = _ckpt(me, "z", z, rows, zcols, dev)
-    yp, ldy = None, 0
     if y is not None:
         yp, ldy = y.data_ptr(), _ld(me, "y", y, (rows, cols), dev)
     wsp, wsn = _work(me, ws, dev)
     h = _on_device(me, dev, stream)
     code = (_lib or load()).fqt_act_fwd(
-        zp, ldz, zc, act, 1 if gated else 0, rows, cols, yp, ldy,
-        _ckpt(me, "z8", z8, rows, zcols, dev), _vec(me, "y_amax", y_amax, 1, dev), wsp, wsn, h)
+        _ACT_FWD(zp, ldz, zc, yp, ldy, _ckpt(me, "z8", z8, rows, zcols, dev),
+                 _vec(me, "y_amax", y_amax, 1, dev), rows, cols, act, 1 if gated else 0), wsp, wsn, h)
     if code:
         raise Fp4Error(code, me)
 
@@ -656,7 +658,8 @@ def fqt_act_bwd(dy: torch.Tensor, z, dz: torch.Tensor, act: int = ACT_SILU, gate
         _bad(me, "dy", dy, "a matrix")
     rows, cols = shape
     zcols = 2 * cols if gated else cols
-    lddy, zp, ldz, zc = _ld(me, "dy", dy, shape, dev), None, 0, None
+    lddy = _ld(me, "dy", dy, shape, dev)
+    zp = ldz = zc = 0
     if isinstance(z, Ckpt8):
         zc = _ckpt(me, "z", z, rows, zcols, dev)
     else:
@@ -664,12 +667,12 @@ def fqt_act_bwd(dy: torch.Tensor, z, dz: torch.Tensor, act: int = ACT_SILU, gate
     lddz = _ld(me, "dz", dz, (rows, zcols), dev)
     dbp = _vec(me, "dbias", dbias, zcols, dev)
     h = _on_device(me, dev, stream)
-    if dbp is not None and ws is None:
+    if dbp and ws is None:
         ws = Workspace.colsum(rows, zcols, device=dy.device)
     wsp, wsn = _work(me, ws, dev)
     code = (_lib or load()).fqt_act_bwd(
-        dy.data_ptr(), lddy, zp, ldz, zc, act, 1 if gated else 0, rows, cols, dz.data_ptr(), lddz, dbp,
-        _vec(me, "dz_amax", dz_amax, 1, dev), wsp, wsn, h)
+        _ACT_BWD(dy.data_ptr(), lddy, zp, ldz, zc, dz.data_ptr(), lddz, dbp,
+                 _vec(me, "dz_amax", dz_amax, 1, dev), rows, cols, act, 1 if gated else 0), wsp, wsn, h)
     if code:
         raise Fp4Error(code, me)
 
@@ -685,23 +688,20 @@ def fp4_gemm_epi(a: QTensor, b: QTensor, out: torch.Tensor, alpha: float = 1.0,
     if a.codes.get_device() != dev or b.codes.get_device() != dev:
         _bad(me, "a and b", a.codes, f"operands on device {dev}")
     ldc = _ld(me, "out", out, (M, N), dev, True)
-    rp, ldr, rt, bt = None, 0, OUT_BF16, OUT_BF16
+    rp = ldr = 0
+    rt = bt = OUT_BF16
     if residual is not None:
         rp, ldr = residual.data_ptr(), _ld(me, "residual", residual, (M, N), dev, True)
         rt = _FLOATS[residual.dtype]
     bp = _vec(me, "bias", bias, N, dev, True)
-    if bp is not None:
+    if bp:
         bt = _FLOATS[bias.dtype]
-    zc = None
-    if z8 is not None:
-        _ckpt(me, "z8", z8, M, N, dev)
-        zc = C.pointer(z8._c)
     h = _on_device(me, dev, stream)
     if ws is None:
         ws = Workspace(M, N, a.cols, device=out.device)
     wsp, wsn = _work(me, ws, dev)
     code = (_lib or load()).fp4_gemm_epi(
-        C.byref(a.c), C.byref(b.c), alpha, C.byref(EpilogueC(bp, rp, ldr, zc, act, bt, rt)),
-        out.data_ptr(), ldc, _FLOATS[out.dtype], _vec(me, "c_amax", c_amax, 1, dev), wsp, wsn, h)
+        C.byref(a.c), C.byref(b.c), alpha,
+        _EPI(bp, rp, ldr, _ckpt(me, "z8", z8, M, N, dev), act, bt, rt), out.data_ptr(), ldc, _FLOATS[out.dtype], _vec(me, "c_amax", c_amax, 1, dev), wsp, wsn, h)
     if code:
         raise Fp4Error(code, me)

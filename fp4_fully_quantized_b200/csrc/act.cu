@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, GATED && DBIAS ? 3 : 4) act_bwd_kern
   amax.to(p.amax);
   if constexpr (DBIAS) {
     // join the CTA's rows, half by half
+    allow_next_launch();
     __shared__ float sums[kThreads * 8];
     const int width = p.lanes * 8;
 #pragma unroll
@@ -299,9 +300,9 @@ using namespace fp4impl;
 
 extern "C" {
 
-fp4_status fqt_act_fwd(const void* z, int64_t ldz, const fqt_ckpt8* z8_in, int32_t act, int32_t gated,
-                       int64_t rows, int64_t cols, void* y, int64_t ldy, const fqt_ckpt8* z8_out,
-                       float* y_amax, void* ws, size_t ws_bytes, void* stream) {
+fp4_status fqt_act_fwd(const fqt_act_fwd_args* args, void* ws, size_t ws_bytes, void* stream) {
+  if (args == nullptr) return FP4_ERR_NULL;
+  const auto& [z, ldz, z8_in, y, ldy, z8_out, y_amax, rows, cols, act, gated] = *args;
   const int64_t zcols = gated ? 2 * cols : cols;
   fp4_status st = check_act(z, ldz, z8_in, act, rows, cols, zcols, ws, ws_bytes);
   if (st != FP4_OK) return st;
@@ -327,9 +328,9 @@ fp4_status fqt_act_fwd(const void* z, int64_t ldz, const fqt_ckpt8* z8_in, int32
   return launch<true>(p, act, gated != 0, slices, s) == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }
 
-fp4_status fqt_act_bwd(const void* dy, int64_t lddy, const void* z, int64_t ldz, const fqt_ckpt8* z8,
-                       int32_t act, int32_t gated, int64_t rows, int64_t cols, void* dz, int64_t lddz,
-                       float* dbias, float* dz_amax, void* ws, size_t ws_bytes, void* stream) {
+fp4_status fqt_act_bwd(const fqt_act_bwd_args* args, void* ws, size_t ws_bytes, void* stream) {
+  if (args == nullptr) return FP4_ERR_NULL;
+  const auto& [dy, lddy, z, ldz, z8, dz, lddz, dbias, dz_amax, rows, cols, act, gated] = *args;
   const int64_t zcols = gated ? 2 * cols : cols;
   fp4_status st = check_act(z, ldz, z8, act, rows, cols, zcols, ws, ws_bytes);
   if (st != FP4_OK) return st;

@@ -89,6 +89,11 @@ inline int64_t colsum_slices(int64_t rows) { return rows < kMaxSlices ? rows : k
 inline float* colsum_partials(void* ws) {
   return reinterpret_cast<float*>(static_cast<char*>(ws) + sizeof(DeviceStatus));
 }
+// Called by the kernels that write the partials when they have few instructions
+// left: the launch of the sum then overlaps their end.
+__device__ __forceinline__ void allow_next_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 cudaError_t launch_colsum(const float* partial, int64_t slices, int64_t cols, float* out,
                           cudaStream_t s);
 

@@ -20,6 +20,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cfloat>
 #include <cstdint>
 #include <type_traits>
@@ -436,6 +437,7 @@ rmsnorm_bwd_kernel(const BwdParams p) {
   }
   if (failed && at.first_warp) ring_give_up(ring, slot, phase, p.status, 0x4200);
   if (p.partial == nullptr) return;
+  allow_next_launch();
   // join the CTA's rows through shared memory (no copies are on their way: every
   // one that was issued has been waited for)
   const int rows_held = at.groups * at.rows_per_tile;
@@ -495,12 +497,26 @@ RowPlan row_plan(int64_t cols, int bytes_per_value, bool row_sums, bool few) {
   return r;
 }
 
+// Lets a kernel take all of an SM's shared memory, once per device (a bit each
+// of `allowed`): half a microsecond of a small call otherwise.
+cudaError_t allow_shared(const void* kernel, std::atomic<uint64_t>& allowed) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (bit != 0 && (allowed.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 1024);
+  if (e == cudaSuccess) allowed.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 template <typename P>
-cudaError_t launch_rows(void (*kernel)(const P), P& p, const RowPlan& r, int grid, cudaStream_t s) {
+cudaError_t launch_rows(void (*kernel)(const P), std::atomic<uint64_t>& allowed, P& p, const RowPlan& r,
+                        int grid, cudaStream_t s) {
   p.T = r.T;
   p.stages = r.stages;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, r.smem);
-  if (e != cudaSuccess) return e;
+  if (const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), allowed); e != cudaSuccess)
+    return e;
   kernel<<<grid, r.threads, r.smem, s>>>(p);
   count_launches(1);
   return cudaGetLastError();
@@ -513,7 +529,11 @@ cudaError_t launch_fwd(FwdParams& p, cudaStream_t s) {
   const int64_t want = (p.rows + r.rows_per_cta - 1) / r.rows_per_cta;
   const int64_t room = (int64_t)sm_count() * r.per_sm;
   const int grid = (int)(want < room ? want : room);
-#define FP4_FWD(W, V, THREADS) return launch_rows(rmsnorm_fwd_kernel<W, V, RES, THREADS>, p, r, grid, s)
+#define FP4_FWD(W, V, THREADS)                                                        \
+  do {                                                                                \
+    static std::atomic<uint64_t> allowed{0};                                          \
+    return launch_rows(rmsnorm_fwd_kernel<W, V, RES, THREADS>, allowed, p, r, grid, s); \
+  } while (0)
   if (r.T == 8) {
     if (r.chunks == 1) FP4_FWD(8, 1, 256);
     if (r.chunks == 2) FP4_FWD(8, 2, 256);
@@ -540,7 +560,11 @@ cudaError_t launch_bwd(BwdParams& p, int& grid, cudaStream_t s) {
   const int64_t want = (p.rows + r.rows_per_cta - 1) / r.rows_per_cta;
   const int64_t room = kMaxSlices / 3 * r.per_sm;
   grid = (int)(want < room ? want : room);
-#define FP4_BWD(W, V, THREADS) return launch_rows(rmsnorm_bwd_kernel<W, V, SRC, GF32, THREADS>, p, r, grid, s)
+#define FP4_BWD(W, V, THREADS)                                                              \
+  do {                                                                                      \
+    static std::atomic<uint64_t> allowed{0};                                                \
+    return launch_rows(rmsnorm_bwd_kernel<W, V, SRC, GF32, THREADS>, allowed, p, r, grid, s); \
+  } while (0)
   if (r.T == 8) {
     if (r.chunks == 1) FP4_BWD(8, 1, 256);
     if (r.chunks == 2) FP4_BWD(8, 2, 256);
@@ -577,11 +601,10 @@ using namespace fp4impl;
 
 extern "C" {
 
-fp4_status fqt_rmsnorm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr,
-                           void* res_out, int64_t ldo, int32_t res_dtype, const void* weight,
-                           int32_t w_dtype, float eps, int64_t rows, int64_t cols, void* y,
-                           int64_t ldy, const fqt_ckpt8* q8, int32_t q8_of, float* rstd,
-                           float* y_amax, void* ws, size_t ws_bytes, void* stream) {
+fp4_status fqt_rmsnorm_fwd(const fqt_rmsnorm_fwd_args* args, void* ws, size_t ws_bytes, void* stream) {
+  if (args == nullptr) return FP4_ERR_NULL;
+  const auto& [x, ldx, residual, ldr, res_out, ldo, weight, y, ldy, q8, rstd, y_amax, rows, cols, eps,
+               res_dtype, w_dtype, q8_of] = *args;
   fp4_status st = check_norm(rows, cols, weight, w_dtype, ws, ws_bytes);
   if (st != FP4_OK) return st;
   if (y == nullptr && q8 == nullptr && rows > 0) return FP4_ERR_NULL;
@@ -615,11 +638,10 @@ fp4_status fqt_rmsnorm_fwd(const void* x, int64_t ldx, const void* residual, int
   return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }
 
-fp4_status fqt_rmsnorm_bwd(const void* dy, int64_t lddy, const void* sum, int64_t lds, int32_t s_dtype,
-                           const fqt_ckpt8* xhat8, const float* rstd, const void* weight,
-                           int32_t w_dtype, const void* dres, int64_t lddres, void* dx, int64_t lddx,
-                           int32_t grad_dtype, int64_t rows, int64_t cols, float* dweight, void* ws,
-                           size_t ws_bytes, void* stream) {
+fp4_status fqt_rmsnorm_bwd(const fqt_rmsnorm_bwd_args* args, void* ws, size_t ws_bytes, void* stream) {
+  if (args == nullptr) return FP4_ERR_NULL;
+  const auto& [dy, lddy, sum, lds, xhat8, rstd, weight, dres, lddres, dx, lddx, dweight, rows, cols,
+               s_dtype, w_dtype, grad_dtype] = *args;
   fp4_status st = check_norm(rows, cols, weight, w_dtype, ws, ws_bytes);
   if (st != FP4_OK) return st;
   if (!known_dtype(grad_dtype)) return FP4_ERR_FORMAT;

@@ -386,11 +386,29 @@ size_t fqt_colsum_workspace_bytes(int64_t rows, int64_t cols);
  * (FQT_RMS_XHAT, the checkpoint fqt_rmsnorm_bwd takes); rstd [rows] float;
  * y_amax [1] float.  The statistics and y come from the unrounded s.
  * cols <= 16384; eps > 0; s^2 must not overflow FP32. */
-fp4_status fqt_rmsnorm_fwd(const void* x_bf16, int64_t ldx, const void* residual, int64_t ldr,
-                           void* res_out, int64_t ldo, int32_t res_dtype, const void* weight,
-                           int32_t w_dtype, float eps, int64_t rows, int64_t cols, void* y_bf16,
-                           int64_t ldy, const fqt_ckpt8* q8, int32_t q8_of, float* rstd,
-                           float* y_amax, void* ws, size_t ws_bytes, void* stream);
+typedef struct fqt_rmsnorm_fwd_args {
+  const void* x;              /* BF16 [rows, ldx]                       */
+  int64_t ldx;
+  const void* residual;       /* res_dtype [rows, ldr], or NULL         */
+  int64_t ldr;
+  void* res_out;              /* res_dtype [rows, ldo], or NULL         */
+  int64_t ldo;
+  const void* weight;         /* w_dtype [cols]                         */
+  void* y;                    /* BF16 [rows, ldy], or NULL              */
+  int64_t ldy;
+  const fqt_ckpt8* q8;        /* or NULL                                */
+  float* rstd;                /* or NULL                                */
+  float* y_amax;              /* or NULL                                */
+  int64_t rows;
+  int64_t cols;
+  float eps;
+  int32_t res_dtype;          /* FP4_OUT_BF16 / FP4_OUT_F32             */
+  int32_t w_dtype;
+  int32_t q8_of;              /* FQT_RMS_Y / FQT_RMS_XHAT               */
+} fqt_rmsnorm_fwd_args;
+
+fp4_status fqt_rmsnorm_fwd(const fqt_rmsnorm_fwd_args* args, void* ws, size_t ws_bytes,
+                           void* stream);
 
 /* Its backward: with g = dy * weight,
  *   dx = rstd * (g - xhat * mean_c(g * xhat)) + dres,
@@ -401,11 +419,28 @@ fp4_status fqt_rmsnorm_fwd(const void* x_bf16, int64_t ldx, const void* residual
  * two.  dy BF16; dres (nullable, the gradient arriving along the residual
  * stream) and dx of type grad_dtype, dx may be dres.  With dweight, ws must
  * hold fqt_colsum_workspace_bytes(rows, cols). */
-fp4_status fqt_rmsnorm_bwd(const void* dy_bf16, int64_t lddy, const void* s, int64_t lds,
-                           int32_t s_dtype, const fqt_ckpt8* xhat8, const float* rstd,
-                           const void* weight, int32_t w_dtype, const void* dres, int64_t lddres,
-                           void* dx, int64_t lddx, int32_t grad_dtype, int64_t rows, int64_t cols,
-                           float* dweight, void* ws, size_t ws_bytes, void* stream);
+typedef struct fqt_rmsnorm_bwd_args {
+  const void* dy;             /* BF16 [rows, lddy]                      */
+  int64_t lddy;
+  const void* s;              /* s_dtype [rows, lds], or NULL           */
+  int64_t lds;
+  const fqt_ckpt8* xhat8;     /* or NULL                                */
+  const float* rstd;          /* [rows]                                 */
+  const void* weight;         /* w_dtype [cols]                         */
+  const void* dres;           /* grad_dtype [rows, lddres], or NULL     */
+  int64_t lddres;
+  void* dx;                   /* grad_dtype [rows, lddx]                */
+  int64_t lddx;
+  float* dweight;             /* [cols], or NULL                        */
+  int64_t rows;
+  int64_t cols;
+  int32_t s_dtype;            /* FP4_OUT_BF16 / FP4_OUT_F32             */
+  int32_t w_dtype;
+  int32_t grad_dtype;
+} fqt_rmsnorm_bwd_args;
+
+fp4_status fqt_rmsnorm_bwd(const fqt_rmsnorm_bwd_args* args, void* ws, size_t ws_bytes,
+                           void* stream);
 
 /* Activation forward.  gated == 0: y = act(z), z [rows, cols]; gated != 0:
  * y = act(z[:, :cols]) * z[:, cols:], z [rows, 2 cols].  z comes as BF16 (`z`,
@@ -413,10 +448,21 @@ fp4_status fqt_rmsnorm_bwd(const void* dy_bf16, int64_t lddy, const void* s, int
  * y; with FQT_ACT_NONE the checkpoint's decoding): exactly one of the two.
  * Outputs: y BF16 [rows, cols]; z8_out the checkpoint of a BF16 z (with y
  * NULL: encoding alone); y_amax.  y or z8_out is needed, y_amax needs y. */
-fp4_status fqt_act_fwd(const void* z_bf16, int64_t ldz, const fqt_ckpt8* z8_in, int32_t act,
-                       int32_t gated, int64_t rows, int64_t cols, void* y_bf16, int64_t ldy,
-                       const fqt_ckpt8* z8_out, float* y_amax, void* ws, size_t ws_bytes,
-                       void* stream);
+typedef struct fqt_act_fwd_args {
+  const void* z;              /* BF16 [rows, ldz], or NULL              */
+  int64_t ldz;
+  const fqt_ckpt8* z8_in;     /* or NULL                                */
+  void* y;                    /* BF16 [rows, ldy], or NULL              */
+  int64_t ldy;
+  const fqt_ckpt8* z8_out;    /* or NULL                                */
+  float* y_amax;              /* or NULL                                */
+  int64_t rows;
+  int64_t cols;               /* of y                                   */
+  int32_t act;                /* FQT_ACT_*                              */
+  int32_t gated;
+} fqt_act_fwd_args;
+
+fp4_status fqt_act_fwd(const fqt_act_fwd_args* args, void* ws, size_t ws_bytes, void* stream);
 
 /* Its backward: dz = dy * act'(z), or [dy * z[:, cols:] * act'(z[:, :cols]),
  * dy * act(z[:, :cols])] when gated; z as above.  dy BF16 [rows, cols]; dz
@@ -424,10 +470,23 @@ fp4_status fqt_act_fwd(const void* z_bf16, int64_t ldz, const fqt_ckpt8* z8_in, 
  * [z's row length], overwritten with the sums of the unrounded dz over the
  * rows; dz_amax nullable.  act' of ReLU at 0 is 0.  With dbias, ws must hold
  * fqt_colsum_workspace_bytes(rows, z's row length). */
-fp4_status fqt_act_bwd(const void* dy_bf16, int64_t lddy, const void* z_bf16, int64_t ldz,
-                       const fqt_ckpt8* z8, int32_t act, int32_t gated, int64_t rows, int64_t cols,
-                       void* dz_bf16, int64_t lddz, float* dbias, float* dz_amax, void* ws,
-                       size_t ws_bytes, void* stream);
+typedef struct fqt_act_bwd_args {
+  const void* dy;             /* BF16 [rows, lddy]                      */
+  int64_t lddy;
+  const void* z;              /* BF16 [rows, ldz], or NULL              */
+  int64_t ldz;
+  const fqt_ckpt8* z8;        /* or NULL                                */
+  void* dz;                   /* BF16 [rows, lddz]                      */
+  int64_t lddz;
+  float* dbias;               /* [z's row length], or NULL              */
+  float* dz_amax;             /* or NULL                                */
+  int64_t rows;
+  int64_t cols;               /* of dy                                  */
+  int32_t act;                /* FQT_ACT_*                              */
+  int32_t gated;
+} fqt_act_bwd_args;
+
+fp4_status fqt_act_bwd(const fqt_act_bwd_args* args, void* ws, size_t ws_bytes, void* stream);
 
 /* fp4_gemm with an epilogue on its FP32 result P (as fp4_gemm computes it):
  *   z = P + bias[n],  C = act(z) + residual,

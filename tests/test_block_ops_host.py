@@ -84,30 +84,33 @@ def test_block_format_by_search():
                 assert abs(values[r, i]) == table[even]
 
 
-P = lambda n: C.c_void_p(n << 20)                    # fake, aligned, never dereferenced
+P = lambda n: n << 20                                # fake, aligned, never dereferenced
+_kept = []
 
 
 def _ck(rows, cols, codes=7, scales=8):
-    return C.byref(F.Ckpt8C(codes << 20 if codes else None, scales << 20 if scales else None, rows, cols))
+    _kept.append(F.Ckpt8C(codes << 20 if codes else None, scales << 20 if scales else None, rows, cols))
+    return C.addressof(_kept[-1])
 
 
 def _fwd(lib, **o):
-    a = dict(x=P(1), ldx=64, res=P(2), ldr=64, out=P(3), ldo=64, rt=0, w=P(4), wt=0, eps=1e-6, rows=4,
-             cols=64, y=P(5), ldy=64, q=None, of=0, rstd=None, amax=None, ws=None, n=0)
+    ws, n = o.pop("ws", None), o.pop("n", 0)
+    a = dict(x=P(1), ldx=64, res=P(2), ldr=64, out=P(3), ldo=64, w=P(4), y=P(5), ldy=64, q=0, rstd=0,
+             amax=0, rows=4, cols=64, eps=1e-6, rt=0, wt=0, of=0)
     a.update(o)
-    return lib.fqt_rmsnorm_fwd(*a.values(), None)
+    return lib.fqt_rmsnorm_fwd(F._FWD(*a.values()), ws, n, None)
 
 
 @pytest.mark.parametrize("o,code", [
-    (dict(x=None), NULL), (dict(w=None), NULL), (dict(y=None), NULL), (dict(res=None), NULL),
-    (dict(out=None), NULL), (dict(cols=60, ldx=60), SHAPE), (dict(cols=0), SHAPE),
+    (dict(x=0), NULL), (dict(w=0), NULL), (dict(y=0), NULL), (dict(res=0), NULL),
+    (dict(out=0), NULL), (dict(cols=60, ldx=60), SHAPE), (dict(cols=0), SHAPE),
     (dict(cols=16392, ldx=16392), SHAPE), (dict(rows=-1), SHAPE), (dict(ldx=56), SHAPE),
-    (dict(ldy=56), SHAPE), (dict(ldx=68), ALIGN), (dict(x=C.c_void_p((1 << 20) + 2)), ALIGN),
-    (dict(w=C.c_void_p((1 << 20) + 8)), ALIGN), (dict(rt=2), FORMAT), (dict(wt=5), FORMAT),
+    (dict(ldy=56), SHAPE), (dict(ldx=68), ALIGN), (dict(x=(1 << 20) + 2), ALIGN),
+    (dict(w=(1 << 20) + 8), ALIGN), (dict(rt=2), FORMAT), (dict(wt=5), FORMAT),
     (dict(eps=0.0), FORMAT), (dict(eps=float("nan")), FORMAT), (dict(eps=float("inf")), FORMAT),
     (dict(q=_ck(4, 64), of=2), FORMAT), (dict(q=_ck(4, 96)), SHAPE), (dict(q=_ck(5, 64)), SHAPE),
     (dict(q=_ck(4, 64, codes=None)), NULL), (dict(q=_ck(4, 40), cols=40), SHAPE),
-    (dict(amax=C.c_void_p((1 << 20) + 2)), ALIGN), (dict(ws=P(9), n=8), WORKSPACE)])
+    (dict(amax=(1 << 20) + 2), ALIGN), (dict(ws=P(9), n=8), WORKSPACE)])
 def test_rmsnorm_fwd_refusals(lib, o, code):
     n = lib.fp4_kernel_launches()
     assert _fwd(lib, **o) == code
@@ -115,52 +118,54 @@ def test_rmsnorm_fwd_refusals(lib, o, code):
 
 
 def _bwd(lib, **o):
-    a = dict(dy=P(1), lddy=64, s=P(2), lds=64, st=0, q=None, rstd=P(3), w=P(4), wt=0, dres=None, lddr=0,
-             dx=P(5), lddx=64, gt=0, rows=4, cols=64, dw=None, ws=None, n=0)
+    ws, n = o.pop("ws", None), o.pop("n", 0)
+    a = dict(dy=P(1), lddy=64, s=P(2), lds=64, q=0, rstd=P(3), w=P(4), dres=0, lddr=0, dx=P(5), lddx=64,
+             dw=0, rows=4, cols=64, st=0, wt=0, gt=0)
     a.update(o)
-    return lib.fqt_rmsnorm_bwd(*a.values(), None)
+    return lib.fqt_rmsnorm_bwd(F._BWD(*a.values()), ws, n, None)
 
 
 @pytest.mark.parametrize("o,code", [
-    (dict(dy=None), NULL), (dict(s=None), NULL), (dict(rstd=None), NULL), (dict(dx=None), NULL),
-    (dict(w=None), NULL), (dict(q=_ck(4, 64)), FORMAT), (dict(s=None, q=_ck(4, 32)), SHAPE),
+    (dict(dy=0), NULL), (dict(s=0), NULL), (dict(rstd=0), NULL), (dict(dx=0), NULL),
+    (dict(w=0), NULL), (dict(q=_ck(4, 64)), FORMAT), (dict(s=0, q=_ck(4, 32)), SHAPE),
     (dict(st=3), FORMAT), (dict(gt=3), FORMAT), (dict(dres=P(6), lddr=60), SHAPE),
     (dict(dw=P(6)), WORKSPACE), (dict(dw=P(6), ws=P(9), n=256), WORKSPACE),
     (dict(dw=P(6), ws=P(9), n=256 + 4 * 64 * 4 - 1), WORKSPACE),
-    (dict(dw=C.c_void_p((1 << 20) + 1), ws=P(9), n=1 << 20), ALIGN)])
+    (dict(dw=(1 << 20) + 1, ws=P(9), n=1 << 20), ALIGN)])
 def test_rmsnorm_bwd_refusals(lib, o, code):
     assert _bwd(lib, **o) == code
 
 
 def _afwd(lib, **o):
-    a = dict(z=P(1), ldz=128, zi=None, act=4, gated=1, rows=4, cols=64, y=P(2), ldy=64, zo=None, amax=None,
-             ws=None, n=0)
+    ws, n = o.pop("ws", None), o.pop("n", 0)
+    a = dict(z=P(1), ldz=128, zi=0, y=P(2), ldy=64, zo=0, amax=0, rows=4, cols=64, act=4, gated=1)
     a.update(o)
-    return lib.fqt_act_fwd(*a.values(), None)
+    return lib.fqt_act_fwd(F._ACT_FWD(*a.values()), ws, n, None)
 
 
 @pytest.mark.parametrize("o,code", [
-    (dict(z=None), NULL), (dict(y=None), NULL), (dict(y=None, zo=_ck(4, 128), amax=P(6)), NULL),
+    (dict(z=0), NULL), (dict(y=0), NULL), (dict(y=0, zo=_ck(4, 128), amax=P(6)), NULL),
     (dict(act=5), FORMAT), (dict(act=-1), FORMAT), (dict(zi=_ck(4, 128)), FORMAT),
-    (dict(z=None, zi=_ck(4, 64)), SHAPE), (dict(z=None, zi=_ck(4, 128), zo=_ck(4, 128)), FORMAT),
+    (dict(z=0, zi=_ck(4, 64)), SHAPE), (dict(z=0, zi=_ck(4, 128), zo=_ck(4, 128)), FORMAT),
     (dict(ldz=120), SHAPE), (dict(cols=60), SHAPE), (dict(rows=-2), SHAPE),
     (dict(cols=48, ldz=96, zo=_ck(4, 96)), SHAPE),          # a block would span both halves
-    (dict(z=None, cols=48, zi=_ck(4, 96)), SHAPE),
-    (dict(z=C.c_void_p((1 << 20) + 8)), ALIGN), (dict(ws=P(9), n=255), WORKSPACE)])
+    (dict(z=0, cols=48, zi=_ck(4, 96)), SHAPE),
+    (dict(z=(1 << 20) + 8), ALIGN), (dict(ws=P(9), n=255), WORKSPACE)])
 def test_act_fwd_refusals(lib, o, code):
     assert _afwd(lib, **o) == code
 
 
 def _abwd(lib, **o):
-    a = dict(dy=P(1), lddy=64, z=P(2), ldz=128, q=None, act=4, gated=1, rows=4, cols=64, dz=P(3), lddz=128,
-             db=None, amax=None, ws=None, n=0)
+    ws, n = o.pop("ws", None), o.pop("n", 0)
+    a = dict(dy=P(1), lddy=64, z=P(2), ldz=128, q=0, dz=P(3), lddz=128, db=0, amax=0, rows=4, cols=64,
+             act=4, gated=1)
     a.update(o)
-    return lib.fqt_act_bwd(*a.values(), None)
+    return lib.fqt_act_bwd(F._ACT_BWD(*a.values()), ws, n, None)
 
 
 @pytest.mark.parametrize("o,code", [
-    (dict(dy=None), NULL), (dict(z=None), NULL), (dict(dz=None), NULL), (dict(lddz=64), SHAPE),
-    (dict(act=9), FORMAT), (dict(q=_ck(4, 128)), FORMAT), (dict(z=None, q=_ck(3, 128)), SHAPE),
+    (dict(dy=0), NULL), (dict(z=0), NULL), (dict(dz=0), NULL), (dict(lddz=64), SHAPE),
+    (dict(act=9), FORMAT), (dict(q=_ck(4, 128)), FORMAT), (dict(z=0, q=_ck(3, 128)), SHAPE),
     (dict(db=P(6)), WORKSPACE), (dict(db=P(6), ws=P(9), n=256 + 4 * 128 * 4 - 1), WORKSPACE)])
 def test_act_bwd_refusals(lib, o, code):
     assert _abwd(lib, **o) == code
@@ -172,10 +177,10 @@ def _q(rows, cols, fmt=0):
 
 
 def _epi(lib, a=(128, 128), b=(256, 128), c=P(1), ldc=256, out=0, ws=P(9), n=256, none=False, **o):
-    e = F.EpilogueC(None, None, 0, None, 0, 0, 0)
-    for k, v in o.items():
-        setattr(e, k, v)
-    return lib.fp4_gemm_epi(_q(*a), _q(*b), 1.0, None if none else C.byref(e), c, ldc, out, None, ws, n, None)
+    e = dict(bias=0, residual=0, ld_residual=0, z8=0, act=0, bias_dtype=0, residual_dtype=0)
+    e.update(o)
+    return lib.fp4_gemm_epi(_q(*a), _q(*b), 1.0, None if none else F._EPI(*e.values()), c, ldc, out, None, ws, n,
+                            None)
 
 
 @pytest.mark.parametrize("o,code", [
@@ -184,12 +189,17 @@ def _epi(lib, a=(128, 128), b=(256, 128), c=P(1), ldc=256, out=0, ws=P(9), n=256
     (dict(bias=2 << 20, bias_dtype=2), FORMAT), (dict(bias=(2 << 20) + 2), ALIGN),
     (dict(residual=2 << 20, ld_residual=128), SHAPE), (dict(residual=2 << 20, ld_residual=260), ALIGN),
     (dict(residual=2 << 20, ld_residual=256, residual_dtype=-1), FORMAT),
-    (dict(z8=C.pointer(F.Ckpt8C(1 << 20, 1 << 20, 128, 128))), SHAPE),
-    (dict(z8=C.pointer(F.Ckpt8C(None, 1 << 20, 128, 256))), NULL)])
+    (dict(z8=_ck(128, 128)), SHAPE),
+    (dict(z8=_ck(128, 256, codes=None)), NULL)])
 def test_gemm_epi_refusals(lib, o, code):
     n = lib.fp4_kernel_launches()
     assert _epi(lib, **o) == code
     assert lib.fp4_kernel_launches() == n
+
+
+def test_missing_arguments(lib):
+    for f in (lib.fqt_rmsnorm_fwd, lib.fqt_rmsnorm_bwd, lib.fqt_act_fwd, lib.fqt_act_bwd):
+        assert f(None, None, 0, None) == NULL
 
 
 def test_size_helpers(lib):
