@@ -228,24 +228,24 @@ __global__ void __launch_bounds__(kThreads, GATED && DBIAS ? 3 : 4) act_bwd_kern
 int lanes_for(int64_t cols) { return cols <= 64 ? 8 : cols <= 128 ? 16 : 32; }
 
 // Row slices of the grid, for a part of 148 SMs with `per_sm` CTAs each at a time:
-// among up to 64 slices (and no more than there are groups of rows) the
-// one whose last wave is fullest, the fewest of those.  148 is a constant here,
-// so that sums do not depend on the device.
+// the fewest (of up to 64, and no more than there are groups of rows) that fill
+// their waves to 0.96, else those that fill them best; a CTA then has many rows,
+// and there are few partial sums.  148 is a constant here, so that
+// sums do not depend on the device.
 dim3 act_grid(int64_t rows, int64_t cols, int lanes, int per_sm) {
   const int64_t wave = 148 * per_sm;
   const int64_t gx = (cols + lanes * 8 - 1) / (lanes * 8);
   const int64_t groups = (rows + kThreads / lanes - 1) / (kThreads / lanes);
-  const int64_t least = gx >= wave ? 1 : wave / gx;              // one wave at least
-  const int64_t most = least > 64 ? least : 64;
-  int64_t best = 1;
+  const int64_t least = gx >= wave ? 1 : wave / gx;              // one wave, or just under
+  int64_t best = least;
   double full = -1.0;
-  for (int64_t gy = least; gy <= most && gy <= groups && gy <= kMaxSlices; ++gy) {
+  for (int64_t gy = least; gy <= 64 && full < 0.96; ++gy) {
     const int64_t n = gx * gy, waves = (n + wave - 1) / wave;
     const double f = (double)n / (double)(waves * wave);
-    if (f > full + 0.01) { full = f; best = gy; }
+    if (f > full) { full = f; best = gy; }
   }
-  if (full < 0.0) best = groups < kMaxSlices ? groups : kMaxSlices;   // fewer groups than a wave
-  return dim3((unsigned)gx, (unsigned)best);
+  if (best > groups) best = groups;
+  return dim3((unsigned)gx, (unsigned)(best < kMaxSlices ? best : kMaxSlices));
 }
 
 template <bool FWD, int ACT, bool GATED, bool CKPT>

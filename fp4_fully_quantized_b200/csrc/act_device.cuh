@@ -142,26 +142,23 @@ __device__ __forceinline__ f32x2 logistic2(f32x2 t) {
   return pair(rcp_approx(d.x), rcp_approx(d.y));
 }
 
-// The upper normal tail Q(a) = 1 - Phi(a) and e = exp(-a^2/2) at a = min(|z|, 14),
-// by the rational approximation of erfc of Abramowitz and Stegun, Handbook of
-// Mathematical Functions, 7.1.26: for x >= 0 erfc(x) = (a1 t + ... + a5 t^5) *
-// exp(-x^2), t = 1 / (1 + 0.3275911 x), to 1.5e-7, with x = a / sqrt(2): the
-// exponential is the density's too.  An error of 0.75e-7 is one and a quarter
-// units of FP32's last place at 1.  Both reciprocals come from one (of the
-// product: at most 18), because the special functions' pipe, a quarter as wide
-// as the FMA's, would be the bound.
-__device__ __forceinline__ void normal_tail2(float2 z, f32x2& a, f32x2& q, f32x2& e) {
+// Minus the upper normal tail, -Q(a) = Phi(a) - 1, and e = exp(-a^2/2) at
+// a = min(|z|, 14), by the rational approximation of erfc of Abramowitz and
+// Stegun, Handbook of Mathematical Functions, 7.1.26: for x >= 0 erfc(x) =
+// (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), to 1.5e-7, with
+// x = a / sqrt(2): the exponential is the density's too.  An error of 0.75e-7 is
+// one and a quarter units of FP32's last place at 1.
+__device__ __forceinline__ void normal_tail2(float2 z, f32x2& a, f32x2& nq, f32x2& e) {
   a = pair(min_nan(fabsf(z.x), 14.0f), min_nan(fabsf(z.y), 14.0f));
   const float2 d = unpair(fma2(a, both(0.23164190f), both(1.0f)));      // 0.3275911 / sqrt(2)
-  const float r = rcp_approx(d.x * d.y);
-  const f32x2 t = mul2(both(r), pair(d.y, d.x));
+  const f32x2 t = pair(rcp_approx(d.x), rcp_approx(d.y));
   const float2 x = unpair(mul2(mul2(a, both(-0.5f * kLog2e)), a));
   e = pair(ex2_approx(x.x), ex2_approx(x.y));
-  q = fma2(t, both(0.5f * 1.061405429f), both(-0.5f * 1.453152027f));
-  q = fma2(q, t, both(0.5f * 1.421413741f));
-  q = fma2(q, t, both(-0.5f * 0.284496736f));
-  q = fma2(q, t, both(0.5f * 0.254829592f));
-  q = mul2(mul2(q, t), e);
+  f32x2 q = fma2(t, both(-0.5f * 1.061405429f), both(0.5f * 1.453152027f));
+  q = fma2(q, t, both(-0.5f * 1.421413741f));
+  q = fma2(q, t, both(0.5f * 0.284496736f));
+  q = fma2(q, t, both(-0.5f * 0.254829592f));
+  nq = mul2(mul2(q, t), e);
 }
 
 // act(z)
@@ -173,9 +170,9 @@ __device__ __forceinline__ f32x2 act_value2(f32x2 z) {
   if constexpr (ACT == FQT_ACT_SILU) return mul2(z, logistic2(mul2(z, both(-kLog2e))));
   if constexpr (ACT == FQT_ACT_GELU) {
     // z Phi(z) = max(z, 0) - |z| Q(|z|)
-    f32x2 a, q, e;
-    normal_tail2(v, a, q, e);
-    return fma2(mul2(a, both(-1.0f)), q, pair(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
+    f32x2 a, nq, e;
+    normal_tail2(v, a, nq, e);
+    return fma2(a, nq, pair(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
   }
   if constexpr (ACT == FQT_ACT_GELU_TANH) {
     const float2 s = unpair(mul2(z, z));
@@ -200,10 +197,10 @@ __device__ __forceinline__ void act_both2(f32x2 z, f32x2& f, f32x2& df) {
   }
   if constexpr (ACT == FQT_ACT_GELU) {
     // Phi + z phi = 1/2 +- (1/2 - Q) + z phi: beyond |z| = 14 the last is below 2^-126
-    f32x2 a, q, e;
-    normal_tail2(v, a, q, e);
-    f = fma2(mul2(a, both(-1.0f)), q, pair(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
-    const f32x2 odd = fma2(mul2(a, both(0.3989422804014327f)), e, fma2(q, both(-1.0f), both(0.5f)));
+    f32x2 a, nq, e;
+    normal_tail2(v, a, nq, e);
+    f = fma2(a, nq, pair(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
+    const f32x2 odd = fma2(mul2(a, both(0.3989422804014327f)), e, add2(nq, both(0.5f)));
     const float2 o = unpair(odd);
     df = add2(pair(copysignf(o.x, v.x), copysignf(o.y, v.y)), both(0.5f));
   }

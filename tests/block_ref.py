@@ -79,11 +79,11 @@ def act_value_error(z: np.ndarray, kind: str) -> np.ndarray:
     equal to z.
 
     gelu: |z| times the CDF's error.  The tail is q(t) e, q = (a1 t + ... + a5 t^5) / 2
-    (A&S 7.1.26, off by 0.75e-7).  t comes from a reciprocal of a product (two
-    sums and a product rounded, the reciprocal within 2^-23, a product rounded:
-    6 units of 2^-24) and enters with dq/dln t <= (a1 + 2 a2 + 3 a3 + 4 a4 + 5 a5)/2
-    = 1.73; Horner's five steps stay below 0.54, rounded to 2.2 units in all; e is
-    within 4 units and the tail below 1/2: 0.75e-7 + (1.73 * 6 + 2.2 + 2) 2^-24
+    (A&S 7.1.26, off by 0.75e-7).  t comes from a reciprocal (a sum rounded, the
+    reciprocal within 2^-23; 6 units of 2^-24 leave room for a product of two) and
+    enters with dq/dln t <= (a1 + 2 a2 + 3 a3 + 4 a4 + 5 a5)/2 = 1.73; Horner's five
+    steps stay below 0.54, rounded to 2.2 units in all; e is within 4 units and the
+    tail below 1/2: 0.75e-7 + (1.73 * 6 + 2.2 + 2) 2^-24
     = 9.4e-7 < 2^-20."""
     v = np.abs(act(z, kind)[0])
     if kind in ("none", "relu"):
