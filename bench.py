@@ -687,12 +687,13 @@ def run_sweep(args, device):
 
 
 def run_swiglu(device, layers=8, hidden=2048, ffn=8192, tokens=16384, seed=0, check_rows=8,
-               chained=False):
+               chained=False, ckpt8=False):
     """Chained SwiGLU MLP stack through the library's linear layer: NVFP4 fprop
     through all layers (RTN, 16x16 weight tiles), then dgrad / wgrad back with
     stochastically rounded gradients.  Every linear is fqt_linear_fwd /
     fqt_linear_bwd; the SwiGLU glue, silu(g) * u and its derivative, is harness
-    code (torch, FP32 math on BF16 tensors).  The same stack in unquantized FP32
+    code (torch, FP32 math on BF16 tensors), or with `ckpt8` the library's
+    fqt_act_fwd / fqt_act_bwd, which keep gate and up as 8-bit checkpoints.  The same stack in unquantized FP32
     is the comparison.  Returns per-layer relative Frobenius errors of the
     activations, input gradients and both weight gradients, the device time of
     the quantized pass, and the oracle spot check of the first and last layers'
@@ -722,14 +723,20 @@ def run_swiglu(device, layers=8, hidden=2048, ffn=8192, tokens=16384, seed=0, ch
     t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     torch.cuda.synchronize()
     t0.record()
-    h, acts, gus, hin = x0, [], [], []
+    h, acts, gus, hin, z8s = x0, [], [], [], []
     for l in range(L):
         hin.append(h)
         y = torch.empty((M, 2 * Fd), dtype=torch.bfloat16, device=device)
         F.fqt_linear_fwd(cfg, h, w_gu[l], y, sv_gu[l], ws)
-        gu = y.float()
-        gus.append(gu)
-        a = (silu(gu[:, :Fd]) * gu[:, Fd:]).to(torch.bfloat16).contiguous()
+        if ckpt8:
+            gus.append(y)                 # for the checks below; the backward reads z8s
+            z8s.append(F.Ckpt8.empty(M, 2 * Fd, device))
+            a = torch.empty((M, Fd), dtype=torch.bfloat16, device=device)
+            F.fqt_act_fwd(y, a, act=F.ACT_SILU, gated=True, z8=z8s[l], ws=ws)
+        else:
+            gu = y.float()
+            gus.append(gu)
+            a = (silu(gu[:, :Fd]) * gu[:, Fd:]).to(torch.bfloat16).contiguous()
         hin.append(a)
         h = torch.empty((M, H), dtype=torch.bfloat16, device=device)
         F.fqt_linear_fwd(cfg, a, w_d[l], h, sv_d[l], ws)
@@ -760,9 +767,14 @@ def run_swiglu(device, layers=8, hidden=2048, ffn=8192, tokens=16384, seed=0, ch
                 F.fp4_gemm(sv.dyq_t, sv.xq_t, dwd[l], ws=ws)
             else:
                 F.fqt_linear_bwd(cfg, d, sv_d[l], da, dwd[l], ws)
-            g, u = gus[l][:, :Fd], gus[l][:, Fd:]
-            daf = da.float()
-            dgu = torch.cat([daf * u * dsilu(g), daf * silu(g)], dim=1).to(torch.bfloat16).contiguous()
+            if ckpt8:
+                dgu = torch.empty((M, 2 * Fd), dtype=torch.bfloat16, device=device)
+                F.fqt_act_bwd(da, z8s[l], dgu, act=F.ACT_SILU, gated=True, ws=ws)
+            else:
+                g, u = gus[l][:, :Fd], gus[l][:, Fd:]
+                daf = da.float()
+                dgu = torch.cat([daf * u * dsilu(g), daf * silu(g)],
+                                dim=1).to(torch.bfloat16).contiguous()
             dys[(l, "gu")] = dgu
             dx = torch.empty((M, H), dtype=torch.bfloat16, device=device)
             dwg[l] = torch.empty((2 * Fd, H), dtype=torch.float32, device=device)
@@ -923,7 +935,18 @@ def run_swiglu(device, layers=8, hidden=2048, ffn=8192, tokens=16384, seed=0, ch
                     mism += int((codes[int(r)].cpu().numpy() != ref["codes"][0]).sum())
                     mism += int((scales[int(r)].cpu().numpy() != ref["scales"][0]).sum())
                     checked += 1
-    return {"case": "swiglu", "layers": L, "hidden": H, "ffn": Fd, "tokens": M,
+    extra = {}
+    if ckpt8:
+        # what the backward keeps of gate and up, and how far the backward's
+        # dgu is from the one of the BF16 values
+        kept = sum(q.codes.numel() + q.scales.numel() for q in z8s)
+        off = []
+        for l in range(L):
+            g, u, daf = gus[l][:, :Fd].float(), gus[l][:, Fd:].float(), das[l].float()
+            off.append(round(rel(dys[(l, "gu")], torch.cat([daf * u * dsilu(g), daf * silu(g)], dim=1)), 5))
+            del g, u, daf
+        extra = {"ckpt8": {"bytes_kept": kept, "bytes_bf16": 2 * L * M * 2 * Fd, "dgu_rel_err": off}}
+    return {"case": "swiglu", **extra, "layers": L, "hidden": H, "ffn": Fd, "tokens": M,
             "ms_quantized_fwd_bwd": round(ms, 3),
             "tflops_gemm_equiv": round(L * 6 * M * (2 * Fd * H + H * Fd) / (ms * 1e-3) / 1e12, 1),
             "rel_err_vs_fp32": per_layer, "local": local, "chained": chain,
@@ -1155,6 +1178,9 @@ def main():
     ap.add_argument("--chained", action="store_true",
                     help="--case swiglu: also run the backward with each block's dgrad epilogue "
                          "encoding the next block's dY operand (delayed amax)")
+    ap.add_argument("--ckpt8", action="store_true",
+                    help="--case swiglu: gate and up kept as 8-bit checkpoints, the glue by the "
+                         "library's activation calls")
     ap.add_argument("--no-sweep", action="store_true",
                     help="skip the compact quantizer sweep (config 3 at 2^28) after the step")
     ap.add_argument("--e2e-steps", type=int, default=5,
@@ -1180,7 +1206,8 @@ def main():
         elif args.case == "formats":
             print(json.dumps(run_formats(dev, seed=args.seed)), flush=True)
         elif args.case == "swiglu":
-            print(json.dumps(run_swiglu(dev, seed=args.seed, chained=args.chained)), flush=True)
+            print(json.dumps(run_swiglu(dev, seed=args.seed, chained=args.chained,
+                                        ckpt8=args.ckpt8)), flush=True)
         else:
             print(json.dumps(run_case(args, dev)), flush=True)
         return

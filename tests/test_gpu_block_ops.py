@@ -593,3 +593,22 @@ def test_refuses_other_devices_streams_and_aliases(gpu_lib):
         F.fqt_rmsnorm_fwd(x, w, y[:1].expand(4, 64))
     with pytest.raises(F.Fp4Error):                    # too small a workspace
         F.fqt_act_bwd(x, x, y, dbias=torch.zeros(64, device="cuda"), ws=F.Workspace())
+
+
+@pytest.mark.parametrize("chained", [False, True])
+def test_swiglu_stack_with_checkpoints(gpu_lib, chained):
+    """The MLP stack of the bench with its glue by the activation calls, gate
+    and up kept in 8 bits: every linear within its operands' noise, as without;
+    dgu off by what E4M3 loses of gate and up.  Rounding to four significant
+    bits is off by a relative root mean square of 2^-4 / sqrt(3) at most (3.6 %,
+    uniform in half a step of 2^-4 of the value); du carries f(g)'s and dg the
+    root sum of squares of u's and f'(g)'s, of which each is at most about
+    g's: below 2 * 3.6 %."""
+    import bench
+    from test_gpu_swiglu import _check
+    res = bench.run_swiglu(torch.device("cuda", 0), layers=3, hidden=256, ffn=512, tokens=1024, chained=chained,
+                           ckpt8=True)
+    _check(res)
+    c = res["ckpt8"]
+    assert c["bytes_kept"] * 64 == c["bytes_bf16"] * 33
+    assert all(0 < e < 0.072 for e in c["dgu_rel_err"])
