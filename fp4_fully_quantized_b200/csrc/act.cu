@@ -35,8 +35,8 @@ struct ActParams {
   int lanes;
 };
 
-// Where a thread's eight values of z are, row by row, and the values of one row
-// as they are stored.
+// Where a thread's eight values of z are, row by row (`off` columns on: the second
+// half's), and the values of one row as they are stored.
 template <bool CKPT>
 struct Stored;
 template <>
@@ -48,7 +48,7 @@ struct Stored<false> {
     __device__ __forceinline__ void next() { z += step; }
   };
   uint4 q;
-  __device__ __forceinline__ void load(const At& at) { q = ld_stream(at.z); }
+  __device__ __forceinline__ void load(const At& at, int64_t off) { q = ld_stream(at.z + off); }
   __device__ __forceinline__ F8 values() const { return bf16x8(q); }
 };
 template <>
@@ -62,9 +62,9 @@ struct Stored<true> {
   };
   uint2 q;
   uint32_t byte;
-  __device__ __forceinline__ void load(const At& at) {
-    q = ld_stream2(at.codes);
-    byte = *at.scales;
+  __device__ __forceinline__ void load(const At& at, int64_t off) {
+    q = ld_stream2(at.codes + off);
+    byte = at.scales[off >> 5];
   }
   __device__ __forceinline__ F8 values() const { return scaled8(e4m3x8(q), ckpt_scale(byte)); }
 };
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 4) act_fwd_kernel(const ActParams p)
   bool finite = true;
   if (c < p.cols) {
     int64_t row = (int64_t)blockIdx.y * rows_at_once + threadIdx.x / p.lanes;
-    typename Stored<CKPT>::At g_at(p, row, c, step), u_at(p, row, p.cols + c, step);
+    typename Stored<CKPT>::At at(p, row, c, step);
     __nv_bfloat16* out = p.out + row * p.ldo + c;
     uint8_t* codes = p.codes_out + row * p.zcols + c;
     uint8_t* scales = p.scales_out + ((row * p.zcols + c) >> 5);
@@ -93,12 +93,9 @@ __global__ void __launch_bounds__(kThreads, 4) act_fwd_kernel(const ActParams p)
       Stored<CKPT> gs[N], us[N];
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        gs[k].load(g_at);
-        g_at.next();
-        if constexpr (GATED) {
-          us[k].load(u_at);
-          u_at.next();
-        }
+        gs[k].load(at, 0);
+        if constexpr (GATED) us[k].load(at, p.cols);
+        at.next();
       }
 #pragma unroll
       for (int k = 0; k < N; ++k) {
@@ -136,8 +133,13 @@ __global__ void __launch_bounds__(kThreads, 4) act_fwd_kernel(const ActParams p)
   if (!finite) set_status(p.status, FP4_ERR_NONFINITE, 7);
 }
 
+// The backward's CTAs to an SM: as many as have registers for two rows each
+// without spills (16384x8192 SwiGLU from a checkpoint: 0.90 of the copy rate with
+// three, 0.89 with four, 0.86 with five of one row).
+constexpr int bwd_ctas(bool gated, bool ckpt, bool dbias) { return gated && (ckpt || dbias) ? 3 : 4; }
+
 template <int ACT, bool GATED, bool CKPT, bool DBIAS>
-__global__ void __launch_bounds__(kThreads, GATED && DBIAS ? 3 : 4) act_bwd_kernel(const ActParams p) {
+__global__ void __launch_bounds__(kThreads, bwd_ctas(GATED, CKPT, DBIAS)) act_bwd_kernel(const ActParams p) {
   const int lane = threadIdx.x % p.lanes, rows_at_once = kThreads / p.lanes;
   const int64_t c = ((int64_t)blockIdx.x * p.lanes + lane) * 8;
   const int64_t step = (int64_t)gridDim.y * rows_at_once;
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, GATED && DBIAS ? 3 : 4) act_bwd_kern
   F8 db = zero8(), dbu = zero8();
   if (c < p.cols) {
     int64_t row = (int64_t)blockIdx.y * rows_at_once + threadIdx.x / p.lanes;
-    typename Stored<CKPT>::At g_at(p, row, c, step), u_at(p, row, p.cols + c, step);
+    typename Stored<CKPT>::At at(p, row, c, step);
     const __nv_bfloat16* dy_at = p.dy + row * p.lddy + c;
     __nv_bfloat16* out = p.out + row * p.ldo + c;
     const int64_t dy_step = step * p.lddy, out_step = step * p.ldo;
@@ -155,12 +157,9 @@ __global__ void __launch_bounds__(kThreads, GATED && DBIAS ? 3 : 4) act_bwd_kern
       uint4 dys[N];
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        gs[k].load(g_at);
-        g_at.next();
-        if constexpr (GATED) {
-          us[k].load(u_at);
-          u_at.next();
-        }
+        gs[k].load(at, 0);
+        if constexpr (GATED) us[k].load(at, p.cols);
+        at.next();
         dys[k] = ld_stream(dy_at);
         dy_at += dy_step;
       }
@@ -266,7 +265,7 @@ void launch_act(const ActParams& p, bool gated, bool ckpt, dim3 grid, cudaStream
 template <bool FWD>
 cudaError_t launch(ActParams& p, int act, bool gated, unsigned& slices, cudaStream_t s) {
   p.lanes = lanes_for(p.cols);
-  const dim3 grid = act_grid(p.rows, p.cols, p.lanes, !FWD && gated && p.partial != nullptr ? 3 : 4);
+  const dim3 grid = act_grid(p.rows, p.cols, p.lanes, FWD ? 4 : bwd_ctas(gated, p.codes != nullptr, p.partial != nullptr));
   slices = grid.y;
   switch (act) {
     case FQT_ACT_RELU: launch_act<FWD, FQT_ACT_RELU>(p, gated, p.codes != nullptr, grid, s); break;
