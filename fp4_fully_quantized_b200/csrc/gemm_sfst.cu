@@ -1,5 +1,6 @@
 // gemm_sfst.cu -- block-scaled FP4 GEMM with scale factors staged by
-// tcgen05.st (one SM per 128 x 256 output tile).
+// tcgen05.st (one SM per 128 x 256 output tile), and its form with bias,
+// activation, residual and 8-bit checkpoint in the epilogue (EPI).
 //
 // The product is the one of the "FP4" page (How it works: FP4 tensor-core
 // products with higher-precision accumulation).  The design point is how the
@@ -228,7 +229,12 @@ __device__ __forceinline__ uint32_t epilogue32(const StParams& p, int64_t row, i
 
 // Registers of an EPI kernel's warpgroups (four warps each): the epilogue's two
 // hold a row's 128 accumulator columns at once, so that the accumulator is free
-// for the next tile's MMAs before any of the epilogue's arithmetic.  The sum is
+// for the next tile's MMAs before any of the epilogue's arithmetic, which the K
+// loop then hides (32768 x 11008 x 4096 with GELU and checkpoint: 1378 us with the
+// accumulator held through it, 1113 without).  What remains over fp4_gemm's time
+// (0.97 against 0.74 ms there, 1 GB more stores and 20 instructions a value) is the
+// scale stagers' share of the issue slots and, in long runs, the power limit:
+// single launches are 9 % over (8192 x 4096 x 4096: 87 against 79 us).  The sum is
 // what the 512 threads are launched with, 4 x 128.
 constexpr int kEpiRegs = 192, kOtherRegs = 64;
 static_assert(2 * kEpiRegs + 2 * kOtherRegs <= 4 * 128, "register split");
@@ -739,9 +745,11 @@ bool codes_map(CUtensorMap* m, const uint8_t* codes, int64_t rows, int64_t K, ui
 
 }  // namespace
 
-// Tiles of 128 columns instead of 256 where those are at most half the SMs: twice
-// the SMs then share the K loop's operand bytes and the epilogue (128 x 4096 x
-// 4096 with bias and GELU, 16 tiles of 256 columns: 18.0 -> NNN us).  With more tiles the wide ones read fewer operand bytes a flop.
+// Tiles of 128 columns instead of 256 while those are at most half the SMs: twice
+// the SMs then share the epilogue (128 x 4096 x 4096 with bias, GELU and an FP32
+// output, 16 wide tiles: 13.8 us against 17.6; 512 x 4096 x 4096, 64: 13.8 against
+// 16.3).  Beyond, the narrow tiles need a second wave (640 x 4096 x 4096, 80: 20.3
+// against 16.4).  The K loop takes 0.42 us a step of 256 with either.
 static bool narrow_tiles(int64_t tiles_wide) { return tiles_wide * 2 <= sm_count(); }
 
 fp4_status gemm_launch(const GemmArgs& g, cudaStream_t s) {
