@@ -57,13 +57,13 @@ def test_rmsnorm_fwd(gpu_lib, rows, cols, residual, weight):
     x, r, w = _norm_inputs(rows, cols, residual, weight)
     ybuf, y = padded(torch.zeros(rows, cols, dtype=BF16, device="cuda"))
     _, xs = padded(x, 16)
-    res = torch.zeros_like(r) if residual else None
+    rbuf, res = padded(torch.zeros_like(r), 24) if residual else (None, None)
     rstd, amax = torch.zeros(rows, device="cuda"), torch.full((1,), 9e9, device="cuda")
     ws = F.Workspace()
-    F.fqt_rmsnorm_fwd(xs, w, y, residual=r, res_out=res, rstd=rstd, y_amax=amax, eps=eps, ws=ws)
+    F.fqt_rmsnorm_fwd(xs, w, y, residual=padded(r)[1] if residual else None, res_out=res, rstd=rstd, y_amax=amax, eps=eps, ws=ws)
     s, rs, xhat, want = R.rmsnorm(f64(x), f64(r) if residual else None, f64(w), eps)
     if residual:                     # FP32's nearest of the exact sum, then the type's
-        assert torch.equal(res, (x.float() + r.float()).to(r.dtype))
+        assert torch.equal(res, (x.float() + r.float()).to(r.dtype)) and (rbuf[:, cols:] == 7.0).all()
     # rstd: a sum of squares whose every addition is in a chain of at most 64
     # (a tree over threads on top of 32 in one), halved by the root, and two
     # units of rsqrt; y: two products more
@@ -165,7 +165,8 @@ def test_rmsnorm_bwd(gpu_lib, rows, cols, saved, grad, dres, weight):
     dxbuf, dx = padded(torch.zeros(rows, cols, dtype=TYPES[grad], device="cuda"))
     dw = torch.full((cols,), 5.0, device="cuda")
     ws = F.Workspace.colsum(rows, cols)
-    F.fqt_rmsnorm_bwd(padded(dy, 24)[1], w, rstd, dx, dres=dr, dweight=dw, ws=ws, **kw)
+    F.fqt_rmsnorm_bwd(padded(dy, 24)[1], w, rstd, dx, dres=padded(dr, 40)[1] if dres else None, dweight=dw,
+                      ws=ws, **kw)
     want, want_dw = R.rmsnorm_bwd(f64(dy), xhat, f64(rstd), f64(w), f64(dr) if dres else None)
     g, rs = f64(dy) * f64(w), f64(rstd)[:, None]
     # eight roundings along each term, a dot product with chains of at most 64 + 8
