@@ -472,6 +472,7 @@ _FLOATS = {_BF16: OUT_BF16, _F32: OUT_F32}
 # the ten that a small call takes)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _bad(where, name, t, want):
@@ -533,9 +534,9 @@ def _on_device(where, dev, stream):
     launch on the current one."""
     if dev < 0:
         raise ValueError(f"{where}: tensors must be on a CUDA device")
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError(f"{where}: tensors are on device {dev}, the current device is "
-                         f"{torch.cuda.current_device()} (use torch.cuda.device)")
+                         f"{_current_device()} (use torch.cuda.device)")
     if stream is None:
         return _raw_stream(dev)
     if stream.device.index != dev:

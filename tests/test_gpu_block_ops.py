@@ -500,6 +500,43 @@ def test_offsets_past_32_bits(gpu_lib):
     assert (dw == 2).all() and (dx[-1] == 0).all() and (dx[-2] == 0).all()
 
 
+def test_gemm_epi_offsets_past_32_bits(gpu_lib):
+    """Output and checkpoint rows beyond element 2^32 are those of a product of
+    the last rows alone."""
+    F = gpu_lib
+    m, n, k = (1 << 20) + 128, 4096, 64
+    x, w = rand(m, k, seed=1), rand(n, k, seed=2)
+    amax = x.float().abs().max().reshape(1)
+    qa, qb, ql = F.QTensor.empty(m, k), F.QTensor.empty(n, k), F.QTensor.empty(128, k)
+    F.fp4_quantize(x, qa, amax_in=amax)
+    F.fp4_quantize(x[-128:], ql, amax_in=amax)
+    F.fp4_quantize(w, qb)
+    c, z8 = torch.zeros(m, n, dtype=BF16, device="cuda"), F.Ckpt8.empty(m, n)
+    res, bias = c, rand(n, seed=3)                     # the residual in place: zeros
+    F.fp4_gemm_epi(qa, qb, c, bias=bias, act=F.ACT_GELU, residual=res, z8=z8)
+    want, z = torch.zeros(128, n, dtype=BF16, device="cuda"), F.Ckpt8.empty(128, n)
+    F.fp4_gemm_epi(ql, qb, want, bias=bias, act=F.ACT_GELU, z8=z)
+    assert torch.equal(c[-128:], want)
+    assert torch.equal(z8.codes[-128:], z.codes) and torch.equal(z8.scales[-128:], z.scales)
+
+
+def test_explicit_stream(gpu_lib):
+    """stream=: ordered after that stream's earlier work, not the current one's."""
+    F = gpu_lib
+    s, x, y = torch.cuda.Stream(), rand(64, 4096, seed=1), torch.zeros(64, 4096, dtype=BF16, device="cuda")
+    want = torch.zeros_like(y)
+    F.fqt_act_fwd(x, want, act=F.ACT_GELU)
+    src, big = torch.zeros_like(x), torch.zeros(1 << 28, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(8):
+            big.add_(1.0)
+        src.copy_(x)
+    F.fqt_act_fwd(src, y, act=F.ACT_GELU, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+
+
 def _block(F, st):
     """A feed-forward block of a transformer, forward and backward: norm of
     the residual stream with an 8-bit checkpoint, up projection with bias and
