@@ -202,7 +202,7 @@ constexpr int kMaxBars = 8 * kMaxStages;
 // RES: 0 no residual, 1 BF16, 2 FP32.  W: lanes of a warp that share a row; V:
 // chunks of a thread, T * (V - 1) < cols / 8 <= T * V.
 template <int W, int V, int RES, int THREADS>
-__global__ void __launch_bounds__(THREADS, 512 / THREADS)
+__global__ void __launch_bounds__(THREADS, V <= 2 ? 3 : 512 / THREADS)
 rmsnorm_fwd_kernel(const FwdParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float slots[2][16];
@@ -316,7 +316,7 @@ rmsnorm_fwd_kernel(const FwdParams p) {
 // SRC: 0 the stored sum in BF16, 1 in FP32, 2 the 8-bit checkpoint of xhat.
 // GF32: dres and dx in FP32.
 template <int W, int V, int SRC, bool GF32, int THREADS>
-__global__ void __launch_bounds__(THREADS, 512 / THREADS)
+__global__ void __launch_bounds__(THREADS, V <= 2 ? 3 : 512 / THREADS)
 rmsnorm_bwd_kernel(const BwdParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float slots[2][16];
@@ -466,7 +466,8 @@ rmsnorm_bwd_kernel(const BwdParams p) {
 // and writes runs better (32768x4096 with an FP32 residual and a checkpoint, 13
 // bytes: 0.95 of the copy rate against 0.86; 16384x8192, 9 bytes: 0.95 against
 // 0.84); below, 256 threads do not issue fast enough (4 bytes: 0.69 against 0.94;
-// 8 bytes: 0.86 against 0.88).
+// 8 bytes: 0.86 against 0.88).  Short rows (two chunks a thread at most, 80
+// registers) run three CTAs of 256 threads (40001x128: 7.4 us against 8.1 with two).
 struct RowPlan { int T, chunks, threads, rows_per_cta, stages, smem, per_sm; };
 RowPlan row_plan(int64_t cols, int bytes_per_value, bool row_sums, bool few) {
   const int64_t n = cols / 8;
@@ -490,7 +491,7 @@ RowPlan row_plan(int64_t cols, int bytes_per_value, bool row_sums, bool few) {
   };
   const int small = group > 256 ? 1 : 256 / group;
   int64_t stages = few && group <= 256 ? fit((256 + group - 1) / group, 1) : 0;
-  for (int per_sm = 512 / (small * group); per_sm >= 2 && stages < 2; --per_sm) stages = fit(small, per_sm);
+  for (int per_sm = r.chunks <= 2 ? 3 : 512 / (small * group); per_sm >= 2 && stages < 2; --per_sm) stages = fit(small, per_sm);
   for (int groups = (r.T < 32 ? 256 : 512) / group; groups >= 1 && stages < 2; --groups) stages = fit(groups, 1);
   const int sums = row_sums ? r.threads * r.chunks * 8 * 4 : 0;     // the rows' weight sums at the end
   if (r.smem < sums) r.smem = sums;
