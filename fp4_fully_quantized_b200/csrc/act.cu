@@ -76,6 +76,7 @@ constexpr int kRows = 2, kCkptFwdRows = 4;
 
 template <int ACT, bool GATED, bool CKPT>
 __global__ void __launch_bounds__(kThreads, 4) act_fwd_kernel(const ActParams p) {
+  wait_previous_launch();
   const int lane = threadIdx.x % p.lanes, rows_at_once = kThreads / p.lanes;
   const int64_t c = ((int64_t)blockIdx.x * p.lanes + lane) * 8;
   const int64_t step = (int64_t)gridDim.y * rows_at_once;
@@ -128,6 +129,7 @@ __global__ void __launch_bounds__(kThreads, 4) act_fwd_kernel(const ActParams p)
     for (; row + (R - 1) * step < p.rows; row += R * step) body(std::integral_constant<int, R>{});
     for (; row < p.rows; row += step) body(std::integral_constant<int, 1>{});
   }
+  allow_next_launch();
   __syncwarp();
   amax.to(p.amax);
   if (!finite) set_status(p.status, FP4_ERR_NONFINITE, 7);
@@ -140,6 +142,7 @@ constexpr int bwd_ctas(bool gated, bool ckpt, bool dbias) { return gated && (ckp
 
 template <int ACT, bool GATED, bool CKPT, bool DBIAS>
 __global__ void __launch_bounds__(kThreads, bwd_ctas(GATED, CKPT, DBIAS)) act_bwd_kernel(const ActParams p) {
+  wait_previous_launch();
   const int lane = threadIdx.x % p.lanes, rows_at_once = kThreads / p.lanes;
   const int64_t c = ((int64_t)blockIdx.x * p.lanes + lane) * 8;
   const int64_t step = (int64_t)gridDim.y * rows_at_once;
@@ -201,11 +204,11 @@ __global__ void __launch_bounds__(kThreads, bwd_ctas(GATED, CKPT, DBIAS)) act_bw
     for (; row + (kRows - 1) * step < p.rows; row += kRows * step) body(std::integral_constant<int, kRows>{});
     for (; row < p.rows; row += step) body(std::integral_constant<int, 1>{});
   }
+  allow_next_launch();
   __syncwarp();
   amax.to(p.amax);
   if constexpr (DBIAS) {
     // join the CTA's rows, half by half
-    allow_next_launch();
     __shared__ float sums[kThreads * 8];
     const int width = p.lanes * 8;
 #pragma unroll
@@ -248,34 +251,34 @@ dim3 act_grid(int64_t rows, int64_t cols, int lanes, int per_sm) {
 }
 
 template <bool FWD, int ACT, bool GATED, bool CKPT>
-void launch_one(const ActParams& p, dim3 grid, cudaStream_t s) {
-  if constexpr (FWD) act_fwd_kernel<ACT, GATED, CKPT><<<grid, kThreads, 0, s>>>(p);
-  else if (p.partial != nullptr) act_bwd_kernel<ACT, GATED, CKPT, true><<<grid, kThreads, 0, s>>>(p);
-  else act_bwd_kernel<ACT, GATED, CKPT, false><<<grid, kThreads, 0, s>>>(p);
+cudaError_t launch_one(const ActParams& p, dim3 grid, cudaStream_t s) {
+  if constexpr (FWD) return launch_overlapped(act_fwd_kernel<ACT, GATED, CKPT>, grid, kThreads, 0, s, p);
+  else if (p.partial != nullptr)
+    return launch_overlapped(act_bwd_kernel<ACT, GATED, CKPT, true>, grid, kThreads, 0, s, p);
+  else return launch_overlapped(act_bwd_kernel<ACT, GATED, CKPT, false>, grid, kThreads, 0, s, p);
 }
 
 template <bool FWD, int ACT>
-void launch_act(const ActParams& p, bool gated, bool ckpt, dim3 grid, cudaStream_t s) {
-  if (gated && ckpt) launch_one<FWD, ACT, true, true>(p, grid, s);
-  else if (gated) launch_one<FWD, ACT, true, false>(p, grid, s);
-  else if (ckpt) launch_one<FWD, ACT, false, true>(p, grid, s);
-  else launch_one<FWD, ACT, false, false>(p, grid, s);
+cudaError_t launch_act(const ActParams& p, bool gated, bool ckpt, dim3 grid, cudaStream_t s) {
+  if (gated && ckpt) return launch_one<FWD, ACT, true, true>(p, grid, s);
+  if (gated) return launch_one<FWD, ACT, true, false>(p, grid, s);
+  if (ckpt) return launch_one<FWD, ACT, false, true>(p, grid, s);
+  return launch_one<FWD, ACT, false, false>(p, grid, s);
 }
 
 template <bool FWD>
 cudaError_t launch(ActParams& p, int act, bool gated, unsigned& slices, cudaStream_t s) {
+  const bool ckpt = p.codes != nullptr;
   p.lanes = lanes_for(p.cols);
-  const dim3 grid = act_grid(p.rows, p.cols, p.lanes, FWD ? 4 : bwd_ctas(gated, p.codes != nullptr, p.partial != nullptr));
+  const dim3 grid = act_grid(p.rows, p.cols, p.lanes, FWD ? 4 : bwd_ctas(gated, ckpt, p.partial != nullptr));
   slices = grid.y;
   switch (act) {
-    case FQT_ACT_RELU: launch_act<FWD, FQT_ACT_RELU>(p, gated, p.codes != nullptr, grid, s); break;
-    case FQT_ACT_GELU: launch_act<FWD, FQT_ACT_GELU>(p, gated, p.codes != nullptr, grid, s); break;
-    case FQT_ACT_GELU_TANH: launch_act<FWD, FQT_ACT_GELU_TANH>(p, gated, p.codes != nullptr, grid, s); break;
-    case FQT_ACT_SILU: launch_act<FWD, FQT_ACT_SILU>(p, gated, p.codes != nullptr, grid, s); break;
-    default: launch_act<FWD, FQT_ACT_NONE>(p, gated, p.codes != nullptr, grid, s); break;
+    case FQT_ACT_RELU: return launch_act<FWD, FQT_ACT_RELU>(p, gated, ckpt, grid, s);
+    case FQT_ACT_GELU: return launch_act<FWD, FQT_ACT_GELU>(p, gated, ckpt, grid, s);
+    case FQT_ACT_GELU_TANH: return launch_act<FWD, FQT_ACT_GELU_TANH>(p, gated, ckpt, grid, s);
+    case FQT_ACT_SILU: return launch_act<FWD, FQT_ACT_SILU>(p, gated, ckpt, grid, s);
+    default: return launch_act<FWD, FQT_ACT_NONE>(p, gated, ckpt, grid, s);
   }
-  count_launches(1);
-  return cudaGetLastError();
 }
 
 // The checks that both directions make of their shape and of z.

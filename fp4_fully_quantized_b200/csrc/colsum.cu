@@ -20,9 +20,7 @@ constexpr int kColsPerCta = 32, kSlicesAtOnce = 32;
 __global__ void __launch_bounds__(256)
 colsum_kernel(const float* partial, int slices, int64_t cols, float* __restrict__ out) {
   __shared__ float4 acc[kSlicesAtOnce][8];
-  // launched while the kernel that writes the partials still runs: wait for its
-  // end (a wait of the hardware's, on the grid before this one in the stream)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_previous_launch();
   const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
   const int64_t c = (int64_t)blockIdx.x * kColsPerCta + tx * 4;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -37,6 +35,7 @@ colsum_kernel(const float* partial, int slices, int64_t cols, float* __restrict_
     }
   }
   acc[ty][tx] = a;
+  allow_next_launch();
   __syncthreads();
   if (threadIdx.x < kColsPerCta) {
     const int64_t col = (int64_t)blockIdx.x * kColsPerCta + threadIdx.x;
@@ -51,19 +50,8 @@ colsum_kernel(const float* partial, int slices, int64_t cols, float* __restrict_
 
 cudaError_t launch_colsum(const float* partial, int64_t slices, int64_t cols, float* out,
                           cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((cols + kColsPerCta - 1) / kColsPerCta));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, colsum_kernel, partial, (int)slices, cols, out);
-  if (e != cudaSuccess) return e;
-  count_launches(1);
-  return cudaGetLastError();
+  return launch_overlapped(colsum_kernel, dim3((unsigned)((cols + kColsPerCta - 1) / kColsPerCta)), 256, 0, s,
+                           partial, (int)slices, cols, out);
 }
 
 }  // namespace fp4impl

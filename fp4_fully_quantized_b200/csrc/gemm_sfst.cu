@@ -294,6 +294,7 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   if (warp == MMA_WARP) tmem_alloc(smem_u32(tmem_holder), TMEM_COLS);
+  if constexpr (EPI) wait_previous_launch();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -704,6 +705,7 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
     }
   }
 
+  if constexpr (EPI) allow_next_launch();
   tc_fence_before();
   __syncthreads();
   if (warp == MMA_WARP) {
@@ -783,6 +785,9 @@ fp4_status gemm_launch(const GemmArgs& g, cudaStream_t s) {
                    : g.epi ? Tile<256>::EPI_SMEM_BYTES : Tile<256>::SMEM_BYTES;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return FP4_ERR_CUDA;
+  if (g.epi)
+    return launch_overlapped(kernel, dim3((unsigned)grid), NUM_THREADS, (size_t)smem, s, ta, tb, p) == cudaSuccess
+               ? FP4_OK : FP4_ERR_CUDA;
   kernel<<<grid, NUM_THREADS, smem, s>>>(ta, tb, p);
   count_launches(1);
   return cudaGetLastError() == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;

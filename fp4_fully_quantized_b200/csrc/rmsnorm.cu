@@ -165,6 +165,7 @@ __device__ __forceinline__ void ring_start(Ring<N>& ring, uint8_t* smem, uint64_
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  wait_previous_launch();
   __syncthreads();
   if (first_warp)
     for (int i = 0; i < stages; ++i)
@@ -307,6 +308,7 @@ rmsnorm_fwd_kernel(const FwdParams p) {
     if (whole && (tile + 1) * at.rows_per_tile <= p.rows) body(tile, std::true_type{});
     else body(tile, std::false_type{});
   }
+  allow_next_launch();
   if (failed && at.first_warp) ring_give_up(ring, slot, phase, p.status, 0x4100);
   __syncwarp();
   amax.to(p.y_amax);
@@ -435,9 +437,9 @@ rmsnorm_bwd_kernel(const BwdParams p) {
     if (whole && (tile + 1) * at.rows_per_tile <= p.rows) body(tile, std::true_type{});
     else body(tile, std::false_type{});
   }
+  allow_next_launch();
   if (failed && at.first_warp) ring_give_up(ring, slot, phase, p.status, 0x4200);
   if (p.partial == nullptr) return;
-  allow_next_launch();
   // join the CTA's rows through shared memory (no copies are on their way: every
   // one that was issued has been waited for)
   const int rows_held = at.groups * at.rows_per_tile;
@@ -518,9 +520,7 @@ cudaError_t launch_rows(void (*kernel)(const P), std::atomic<uint64_t>& allowed,
   p.stages = r.stages;
   if (const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), allowed); e != cudaSuccess)
     return e;
-  kernel<<<grid, r.threads, r.smem, s>>>(p);
-  count_launches(1);
-  return cudaGetLastError();
+  return launch_overlapped(kernel, dim3((unsigned)grid), r.threads, (size_t)r.smem, s, p);
 }
 
 template <int RES>

@@ -537,6 +537,50 @@ def test_explicit_stream(gpu_lib):
     assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("rows,cols", [(3, 4096), (600, 1024), (4099, 128)])
+def test_calls_in_a_row_see_one_another(gpu_lib, rows, cols):
+    """Launches overlap the end of the kernel before them, so: a chain in which
+    every call reads what the one before wrote and writes what it read, with
+    other kernels in between, gives what it gives with a wait after each."""
+    F = gpu_lib
+    w = rand(cols, seed=1, std=0.1, mean=1.0, dtype=F32)
+    qa, qb = _operands(F, 128, 256, 128, 0)
+
+    def chain(wait):
+        x, r = rand(rows, cols, seed=2), rand(rows, cols, seed=3)
+        y, dx, q8 = torch.zeros_like(x), torch.zeros_like(x), F.Ckpt8.empty(rows, cols)
+        rstd, dw, db = (torch.zeros(n, device="cuda") for n in (rows, cols, cols))
+        c, z8 = rand(128, 256, seed=4), F.Ckpt8.empty(128, 256)
+        amax, ws = torch.zeros(1, device="cuda"), F.Workspace.colsum(rows, cols)
+        total = torch.zeros(cols, device="cuda")
+        steps = [
+            lambda: F.fqt_rmsnorm_fwd(x, w, y, residual=r, res_out=r, q8=q8, q8_of=F.RMS_XHAT, rstd=rstd, ws=ws),
+            lambda: F.fqt_act_fwd(y, x, act=F.ACT_GELU, z8=q8),
+            lambda: F.fqt_act_bwd(x, q8, y, act=F.ACT_GELU, dbias=db, dz_amax=amax, ws=ws),
+            lambda: F.fqt_rmsnorm_bwd(y, w, rstd, dx, s=r, dres=x, dweight=dw, ws=ws),
+            lambda: total.add_(dw).add_(db),
+            lambda: F.fqt_rmsnorm_bwd(dx, w, rstd, dx2, xhat8=q8, dweight=dw, ws=ws),
+            lambda: F.fqt_act_fwd(dx2, x, act=F.ACT_SILU),
+            lambda: F.fp4_gemm_epi(qa, qb, c, alpha=0.01, residual=c, z8=z8),
+            lambda: F.fqt_act_fwd(z8, c, act=F.ACT_GELU_TANH),
+            lambda: F.fp4_gemm_epi(qa, qb, c, alpha=0.01, act=F.ACT_SILU, residual=c),
+            lambda: r.mul_(0.5),
+        ]
+        dx2 = torch.zeros_like(x)
+        for _ in range(25):
+            for step in steps:
+                step()
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return x, y, r, dx, c, total, dw, db, amax, q8.codes, z8.codes
+
+    want = chain(True)
+    assert all(torch.isfinite(t.float()).all() for t in want)
+    for _ in range(4):
+        assert all(torch.equal(a, b) for a, b in zip(chain(False), want))
+
+
 def _block(F, st):
     """A feed-forward block of a transformer, forward and backward: norm of
     the residual stream with an 8-bit checkpoint, up projection with bias and
