@@ -231,10 +231,10 @@ __device__ __forceinline__ uint32_t epilogue32(const StParams& p, int64_t row, i
 // hold a row's 128 accumulator columns at once, so that the accumulator is free
 // for the next tile's MMAs before any of the epilogue's arithmetic, which the K
 // loop then hides (32768 x 11008 x 4096 with GELU and checkpoint: 1378 us with the
-// accumulator held through it, 1113 without).  What remains over fp4_gemm's time
-// (0.97 against 0.74 ms there, 1 GB more stores and 20 instructions a value) is the
-// scale stagers' share of the issue slots and, in long runs, the power limit:
-// single launches are 9 % over (8192 x 4096 x 4096: 87 against 79 us).  The sum is
+// accumulator held through it, 1113 without, 960-990 with the steps below).  What
+// remains over fp4_gemm's time is 6 % more cycles, mostly the checkpoint's stores,
+// and the power limit that long runs reach: 979 us at 1447 MHz against 860 at 1545;
+// single launches take 87 against 79 us (8192 x 4096 x 4096).  The sum is
 // what the 512 threads are launched with, 4 x 128.
 constexpr int kEpiRegs = 192, kOtherRegs = 64;
 static_assert(2 * kEpiRegs + 2 * kOtherRegs <= 4 * 128, "register split");
