@@ -137,8 +137,9 @@ __global__ void __launch_bounds__(kThreads, 4) act_fwd_kernel(const ActParams p)
 
 // The backward's CTAs to an SM: as many as have registers for two rows each
 // without spills (16384x8192 SwiGLU from a checkpoint: 0.90 of the copy rate with
-// three, 0.89 with four, 0.86 with five of one row).
-constexpr int bwd_ctas(bool gated, bool ckpt, bool dbias) { return gated && (ckpt || dbias) ? 3 : 4; }
+// three, 0.89 with four, 0.86 with five of one row; with dbias from BF16 0.90 with
+// two, 0.83 with three).
+constexpr int bwd_ctas(bool gated, bool ckpt, bool dbias) { return gated && dbias ? 2 : gated && ckpt ? 3 : 4; }
 
 template <int ACT, bool GATED, bool CKPT, bool DBIAS>
 __global__ void __launch_bounds__(kThreads, bwd_ctas(GATED, CKPT, DBIAS)) act_bwd_kernel(const ActParams p) {
