@@ -235,6 +235,16 @@ class Workspace:
         w.buf[:256].zero_()
         return w
 
+    @staticmethod
+    def _of_call(make, stream) -> "Workspace":
+        """make() for a call that was given none: allocated and zeroed on the
+        stream its kernels run on, so that the zeroing comes before them, and
+        the memory, free again when the call returns, is next used behind them."""
+        if stream is None:
+            return make()
+        with torch.cuda.stream(stream):
+            return make()
+
     @property
     def ptr(self):
         return C.c_void_p(self.buf.data_ptr())
@@ -274,7 +284,7 @@ def fp4_gemm(a: QTensor, b: QTensor, out: torch.Tensor, alpha: float = 1.0,
     assert out.dtype in (torch.bfloat16, torch.float32) and out.is_cuda and out.stride(1) == 1
     od = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
     if ws is None:
-        ws = Workspace(a.rows, b.rows, a.cols, device=out.device)
+        ws = Workspace._of_call(lambda: Workspace(a.rows, b.rows, a.cols, device=out.device), stream)
     code = load().fp4_gemm(C.byref(a.c), C.byref(b.c), float(alpha), _ptr(out), out.stride(0), od,
                            _ptr(c_amax), ws.ptr, ws.nbytes, _stream(stream))
     _check(code, "fp4_gemm")
@@ -294,7 +304,7 @@ def fp4_gemm_noalloc(a: QTensor, b: QTensor, out: torch.Tensor, alpha: float = 1
 
 def mma_rate(variant: int = 0, iters: int = 20000, stream=None) -> float:
     """Achieved TFLOP/s of back-to-back block-scaled NVFP4 MMAs (see fp4.h)."""
-    ws = Workspace()
+    ws = Workspace._of_call(Workspace, stream)
     out = C.c_float()
     _check(load().fp4_mma_rate(variant, iters, C.byref(out), ws.ptr, ws.nbytes, _stream(stream)),
            "fp4_mma_rate")
@@ -306,7 +316,7 @@ def fp4_gemm_quant(a: QTensor, b: QTensor, out: QTensor, amax_in: torch.Tensor, 
     """out = NVFP4 1x16 RTN of (alpha * s_dec(a) * s_dec(b) * a_hat @ b_hat^T), encoded in
     the GEMM epilogue with the supplied tensor amax (device float32 tensor)."""
     if ws is None:
-        ws = Workspace(a.rows, b.rows, a.cols, device=amax_in.device)
+        ws = Workspace._of_call(lambda: Workspace(a.rows, b.rows, a.cols, device=amax_in.device), stream)
     code = load().fp4_gemm_quant(C.byref(a.c), C.byref(b.c), float(alpha), _ptr(amax_in),
                                  C.byref(out.c), _ptr(c_amax), ws.ptr, ws.nbytes, _stream(stream))
     _check(code, "fp4_gemm_quant")
@@ -319,7 +329,7 @@ def fp4_gemm_quant_ex(a: QTensor, b: QTensor, out: QTensor, amax_in: torch.Tenso
     """fp4_gemm_quant with RTN or SR encoding and an optional BF16 copy of the
     FP32 result (c_bf16, [M, >= N] BF16 CUDA tensor)."""
     if ws is None:
-        ws = Workspace(a.rows, b.rows, a.cols, device=amax_in.device)
+        ws = Workspace._of_call(lambda: Workspace(a.rows, b.rows, a.cols, device=amax_in.device), stream)
     if c_bf16 is not None:
         assert c_bf16.dtype == torch.bfloat16 and c_bf16.is_cuda and c_bf16.stride(1) == 1
     code = load().fp4_gemm_quant_ex(C.byref(a.c), C.byref(b.c), float(alpha), _ptr(amax_in),
@@ -608,7 +618,7 @@ def fqt_rmsnorm_bwd(dy: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, 
     dwp = _vec(me, "dweight", dweight, cols, dev)
     h = _on_device(me, dev, stream)
     if dwp and ws is None:
-        ws = Workspace.colsum(rows, cols, device=dy.device)
+        ws = Workspace._of_call(lambda: Workspace.colsum(rows, cols, device=dy.device), stream)
     wsp, wsn = _work(me, ws, dev)
     code = (_lib or load()).fqt_rmsnorm_bwd(
         _BWD(dy.data_ptr(), lddy, sp, lds, _ckpt(me, "xhat8", xhat8, rows, cols, dev),
@@ -669,7 +679,7 @@ def fqt_act_bwd(dy: torch.Tensor, z, dz: torch.Tensor, act: int = ACT_SILU, gate
     dbp = _vec(me, "dbias", dbias, zcols, dev)
     h = _on_device(me, dev, stream)
     if dbp and ws is None:
-        ws = Workspace.colsum(rows, zcols, device=dy.device)
+        ws = Workspace._of_call(lambda: Workspace.colsum(rows, zcols, device=dy.device), stream)
     wsp, wsn = _work(me, ws, dev)
     code = (_lib or load()).fqt_act_bwd(
         _ACT_BWD(dy.data_ptr(), lddy, zp, ldz, zc, dz.data_ptr(), lddz, dbp,
@@ -699,7 +709,7 @@ def fp4_gemm_epi(a: QTensor, b: QTensor, out: torch.Tensor, alpha: float = 1.0,
         bt = _FLOATS[bias.dtype]
     h = _on_device(me, dev, stream)
     if ws is None:
-        ws = Workspace(M, N, a.cols, device=out.device)
+        ws = Workspace._of_call(lambda: Workspace(M, N, a.cols, device=out.device), stream)
     wsp, wsn = _work(me, ws, dev)
     code = (_lib or load()).fp4_gemm_epi(
         C.byref(a.c), C.byref(b.c), alpha,

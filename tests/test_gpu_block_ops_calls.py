@@ -1,0 +1,68 @@
+"""Calls around the FP4 linear that their documentation allows and that
+tests/test_gpu_block_ops.py does not make."""
+import numpy as np
+import pytest
+import torch
+
+import block_ref as R
+from block_ref import EPS16, EPS32, f64
+from test_gpu_block_ops import BF16, F32, STEP, TINY, TYPES, _act_of, _norm_inputs, _operands, padded, rand
+
+pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------------------
+# A workspace that the call makes itself, on a stream that is not the current one
+# --------------------------------------------------------------------------
+def _behind_work(stream, call):
+    """Runs call(stream) behind a few milliseconds of that stream's work; until
+    they are over, the current stream allocates and writes as much as the
+    allocator has free."""
+    big = torch.zeros(1 << 28, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        for _ in range(16):
+            big.add_(1.0)
+    call(stream)
+    kept = []
+    for n in (256, 1 << 14, 1 << 18, 1 << 20, 1 << 22):
+        kept += [torch.full((n,), 3.0e9, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all((t == 3.0e9).all() for t in kept)         # nor did the call write there
+
+
+@pytest.mark.parametrize("call", ["norm", "act", "gated"])
+def test_row_sums_on_another_stream_without_workspace(gpu_lib, call):
+    F = gpu_lib
+    rows, cols = 2049, 2048
+    dy, x, w = rand(rows, cols, seed=1), rand(rows, 2 * cols, seed=2), torch.ones(cols, device="cuda")
+    dx, rstd = torch.zeros(rows, 2 * cols, dtype=BF16, device="cuda"), torch.ones(rows, device="cuda")
+    sums, want = (torch.zeros(2 * cols if call == "gated" else cols, device="cuda") for _ in range(2))
+
+    def run(out, **k):
+        if call == "norm":
+            F.fqt_rmsnorm_bwd(dy, w, rstd, dx[:, :cols], s=x[:, :cols], dweight=out, **k)
+        else:
+            zc = 2 * cols if call == "gated" else cols
+            F.fqt_act_bwd(dy, x[:, :zc], dx[:, :zc], act=F.ACT_SILU, gated=call == "gated", dbias=out, **k)
+
+    run(want, ws=F.Workspace.colsum(rows, 2 * cols))
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        sums.zero_()
+        _behind_work(s, lambda stream: run(sums, stream=stream))
+        assert torch.equal(sums, want)
+
+
+def test_gemm_epi_on_another_stream_without_workspace(gpu_lib):
+    """A block with Inf is recorded in the call's own workspace, not in memory
+    that the allocator gave away since."""
+    F = gpu_lib
+    qa, qb = _operands(F, 128, 256, 128, 0)
+    bias = torch.full((256,), float("inf"), device="cuda")
+    z8, c = F.Ckpt8.empty(128, 256), torch.zeros(128, 256, dtype=BF16, device="cuda")
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        c.zero_()
+        _behind_work(s, lambda stream: F.fp4_gemm_epi(qa, qb, c, bias=bias, z8=z8, stream=stream))
+        assert torch.isinf(c).all() and (z8.scales == 255).all()
