@@ -455,15 +455,24 @@ def fqt_linear_bwd(cfg: LinearCfgC, dy: torch.Tensor, saved: Saved, dx: torch.Te
 @dataclass
 class Ckpt8:
     """An 8-bit checkpoint of a [rows, cols] tensor: E4M3 codes [rows, cols]
-    and one E8M0 scale per 32 columns, scales [rows, cols // 32] (both as
-    bytes; views as torch.float8_e4m3fn / torch.float8_e8m0fnu are their
-    values)."""
+    and one E8M0 scale per 32 columns, scales [rows, cols // 32] (dense, as
+    bytes or as torch.float8_e4m3fn / torch.float8_e8m0fnu, which are their
+    values).  The fields may be assigned: a call uses the tensors that are in
+    them then."""
     rows: int
     cols: int
     codes: torch.Tensor
     scales: torch.Tensor
-    _c: Ckpt8C = field(default=None, repr=False)
-    _address: int = field(default=0, repr=False)       # of _c
+    # the C structure that the last call got, its address and (_at) what it says:
+    # _ckpt makes another when that is no longer so
+    _c: Ckpt8C = field(default=None, repr=False, compare=False)
+    _address: int = field(default=0, repr=False, compare=False)
+
+    def __post_init__(self):
+        self._c, self._address, self._at = None, 0, None      # none yet, or another object's
+
+    def __reduce__(self):
+        return Ckpt8, (self.rows, self.cols, self.codes, self.scales)
 
     @staticmethod
     def empty(rows: int, cols: int, device="cuda") -> "Ckpt8":
@@ -472,8 +481,7 @@ class Ckpt8:
         dev = torch.device(device)
         codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
         scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
-        c = Ckpt8C(codes.data_ptr(), scales.data_ptr(), rows, cols)
-        return Ckpt8(rows, cols, codes, scales, c, C.addressof(c))
+        return Ckpt8(rows, cols, codes, scales)
 
 
 _BF16, _F32 = torch.bfloat16, torch.float32
@@ -522,12 +530,24 @@ def _vec(where, name, t, n, dev, bf16=False):
     _bad(where, name, t, f"a dense vector of {n} FP32{' or BF16' if bf16 else ''} on device {dev}")
 
 
+def _bytes(where, name, part, t, rows, cols, fp8, dev):
+    if not isinstance(t, torch.Tensor) or t.shape != (rows, cols) or t.get_device() != dev or \
+            not t.is_contiguous() or t.dtype not in (torch.uint8, fp8):
+        _bad(where, f"{name}.{part}", t, f"a dense [{rows}, {cols}] tensor of bytes on device {dev}")
+
+
 def _ckpt(where, name, q, rows, cols, dev):
     """Address of a checkpoint's structure, 0 for None."""
     if q is None:
         return 0
-    if not isinstance(q, Ckpt8) or q.rows != rows or q.cols != cols or q.codes.get_device() != dev:
-        _bad(where, name, q, f"a Ckpt8 of [{rows}, {cols}] on device {dev}")
+    if not isinstance(q, Ckpt8) or q.rows != rows or q.cols != cols:
+        _bad(where, name, q, f"a Ckpt8 of [{rows}, {cols}]")
+    _bytes(where, name, "codes", q.codes, rows, cols, torch.float8_e4m3fn, dev)
+    _bytes(where, name, "scales", q.scales, rows, cols // 32, torch.float8_e8m0fnu, dev)
+    at = (q.codes.data_ptr(), q.scales.data_ptr(), rows, cols)
+    if q._at != at:
+        q._c = Ckpt8C(*at)
+        q._address, q._at = C.addressof(q._c), at
     return q._address
 
 
@@ -637,9 +657,9 @@ def fqt_act_fwd(z, y: torch.Tensor | None = None, act: int = ACT_SILU, gated: bo
     me = "fqt_act_fwd"
     zp = ldz = zc = yp = ldy = 0
     src = z.codes if isinstance(z, Ckpt8) else z
-    dev, zshape = src.get_device(), src.shape
-    if len(zshape) != 2 or (gated and zshape[1] % 2):
+    if not isinstance(src, torch.Tensor) or src.dim() != 2 or (gated and src.shape[1] % 2):
         _bad(me, "z", src, "a matrix, with an even row length when gated")
+    dev, zshape = src.get_device(), src.shape
     rows, zcols = zshape
     cols = zcols // 2 if gated else zcols
     if src is z:

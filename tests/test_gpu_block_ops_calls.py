@@ -66,3 +66,43 @@ def test_gemm_epi_on_another_stream_without_workspace(gpu_lib):
         c.zero_()
         _behind_work(s, lambda stream: F.fp4_gemm_epi(qa, qb, c, bias=bias, z8=z8, stream=stream))
         assert torch.isinf(c).all() and (z8.scales == 255).all()
+
+
+# --------------------------------------------------------------------------
+# Checkpoints whose tensors are not those they were made with
+# --------------------------------------------------------------------------
+def test_checkpoint_brought_back(gpu_lib):
+    """Codes and scales moved off the device and back, into an object of their
+    own or the old one, decode to what they held."""
+    F = gpu_lib
+    z = rand(33, 256, seed=1)
+    q, y, want = F.Ckpt8.empty(33, 256), torch.zeros_like(z), torch.zeros_like(z)
+    F.fqt_act_fwd(z, act=F.ACT_NONE, z8=q)
+    F.fqt_act_fwd(q, want, act=F.ACT_NONE)
+    codes, scales = q.codes.cpu(), q.scales.cpu()
+    again = F.Ckpt8(33, 256, codes.cuda(), scales.cuda())
+    F.fqt_act_fwd(again, y, act=F.ACT_NONE)
+    assert torch.equal(y, want)
+    q.codes.zero_()
+    q.codes, q.scales = codes.cuda(), scales.cuda()
+    y.zero_()
+    F.fqt_act_fwd(q, y, act=F.ACT_NONE)
+    assert torch.equal(y, want)
+    # written through the constructor's object: both tensors, by each call that writes one
+    for made in (lambda c: F.fqt_act_fwd(z, y, z8=c, act=F.ACT_NONE),
+                 lambda c: F.fqt_rmsnorm_fwd(z, torch.ones(256, device="cuda"), y, q8=c)):
+        old = F.Ckpt8.empty(33, 256)
+        made(old)
+        new = F.Ckpt8(33, 256, torch.zeros_like(old.codes), torch.zeros_like(old.scales))
+        made(new)
+        assert torch.equal(new.codes, old.codes) and torch.equal(new.scales, old.scales)
+
+
+def test_checkpoint_on_the_host_is_refused(gpu_lib):
+    F = gpu_lib
+    z = rand(33, 256, seed=1)
+    for part in ("codes", "scales"):
+        q = F.Ckpt8.empty(33, 256)
+        setattr(q, part, getattr(q, part).cpu())
+        with pytest.raises(ValueError):
+            F.fqt_act_fwd(z, act=F.ACT_NONE, z8=q)
