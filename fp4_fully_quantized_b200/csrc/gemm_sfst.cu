@@ -198,7 +198,7 @@ __device__ __forceinline__ uint32_t epilogue32(const StParams& p, int64_t row, i
   }
   if (p.c_amax != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));
+    for (int i = 0; i < 32; i += 2) amax = fp4dev::max_abs3(amax, v[i], v[i + 1]);   // NaN stays
   }
   if (p.out_mode == 1) {
     float* d = static_cast<float*>(p.c) + row * p.ldc + col;
@@ -602,9 +602,15 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
       }
     }
     if (p.c_amax != nullptr) {
+      if constexpr (EPI) {
+        // as bits without the sign: they order by magnitude, NaN on top
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, fp4dev::abs_bits(amax));
+        if (lane == 0) atomicMax(reinterpret_cast<unsigned int*>(p.c_amax), top);
+      } else {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-      if (lane == 0) atomicMax(reinterpret_cast<unsigned int*>(p.c_amax), __float_as_uint(amax));
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        if (lane == 0) atomicMax(reinterpret_cast<unsigned int*>(p.c_amax), __float_as_uint(amax));
+      }
     }
   } else {
     fewer_registers<EPI>();

@@ -348,9 +348,10 @@ fp4_status fp4_quant_noise(const void* x_bf16, int64_t rows, int64_t cols, int64
 /* alone.  `ws` may be NULL where no workspace size is asked for (device     */
 /* conditions are then not recorded); calls that may run at the same time,   */
 /* replays of captured graphs among them, need workspaces of their own.      */
-/* amax outputs are max |v| of the values as stored in BF16, so that          */
+/* y_amax and dz_amax are max |v| of the values as stored in BF16, so that    */
 /* fp4_quantize with that amax_in gives the bits that it gives with its own   */
-/* amax pass; a NaN or Inf among the values shows in the amax.                */
+/* amax pass; fp4_gemm_epi's c_amax is of its FP32 values.  A NaN or Inf      */
+/* among the values shows in the amax.                                        */
 /* ---------------------------------------------------------------------- */
 enum { FQT_ACT_NONE = 0, FQT_ACT_RELU = 1, FQT_ACT_GELU = 2, FQT_ACT_GELU_TANH = 3,
        FQT_ACT_SILU = 4 };                        /* GELU: z Phi(z); _TANH its tanh form */
@@ -494,7 +495,8 @@ fp4_status fqt_act_bwd(const fqt_act_bwd_args* args, void* ws, size_t ws_bytes, 
  * start a multiple of 16 bytes; it may be c itself when type and leading
  * dimension agree) may each be NULL and are of the given types; z8 (nullable)
  * receives the checkpoint of z, [M, N], which fqt_act_bwd takes.  c_amax
- * receives max |C| of the FP32 values.  All else as fp4_gemm. */
+ * receives max |C| of the FP32 values, NaN when one of them is (fp4_gemm's
+ * leaves NaN out).  All else as fp4_gemm. */
 typedef struct fp4_epilogue {
   const void* bias;
   const void* residual;

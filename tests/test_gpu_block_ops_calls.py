@@ -106,3 +106,44 @@ def test_checkpoint_on_the_host_is_refused(gpu_lib):
         setattr(q, part, getattr(q, part).cpu())
         with pytest.raises(ValueError):
             F.fqt_act_fwd(z, act=F.ACT_NONE, z8=q)
+
+
+# --------------------------------------------------------------------------
+# The GEMM's amax of values that are not finite
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("m,n", [(128, 256), (1280, 2176)])       # narrow tiles, wide ones
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["none", "relu", "gelu"])
+def test_gemm_epi_amax_of_nonfinite_values(gpu_lib, m, n, out, kind):
+    """A NaN or Inf of the bias or the residual is in C and in c_amax, without a
+    checkpoint too; a NaN outweighs Inf."""
+    F = gpu_lib
+    qa, qb = _operands(F, m, n, 128, 0)
+    c, amax = torch.zeros(m, n, dtype=TYPES[out], device="cuda"), torch.zeros(1, device="cuda")
+    act = _act_of(F, kind)
+    bias, res = torch.zeros(n, device="cuda"), torch.zeros(m, n, dtype=BF16, device="cuda")
+    F.fp4_gemm_epi(qa, qb, c, bias=bias, act=act, residual=res, c_amax=amax)
+    finite = float(amax)
+    assert finite == float(c.abs().max()) or out == "bf16"        # the FP32 values' maximum
+    for value in (float("nan"), float("inf")):
+        for col in (0, n - 1, 70):
+            bias.zero_()
+            bias[col] = value
+            F.fp4_gemm_epi(qa, qb, c, bias=bias, act=act, c_amax=amax)
+            bad = torch.isnan(c) if value != value else torch.isinf(c)
+            assert bad[:, col].all() and int(bad.sum()) == m
+            assert np.isnan(float(amax)) if value != value else float(amax) == value
+    for row, col in ((0, 0), (m - 1, n - 1), (77, 33)):
+        res.zero_()
+        res[row, col] = float("nan")
+        F.fp4_gemm_epi(qa, qb, c, act=act, residual=res, c_amax=amax)
+        assert int(torch.isnan(c).sum()) == 1 and torch.isnan(c[row, col]) and np.isnan(float(amax))
+        res[row, col] = -float("inf")
+        F.fp4_gemm_epi(qa, qb, c, act=act, residual=res, c_amax=amax)
+        assert float(amax) == float("inf")
+    bias.fill_(float("inf"))
+    res[5, 5] = float("nan")
+    F.fp4_gemm_epi(qa, qb, c, bias=bias, act=act, residual=res, c_amax=amax)
+    assert np.isnan(float(amax))
+    F.fp4_gemm_epi(qa, qb, c, act=act, c_amax=amax)                # and the next call's is its own
+    assert float(amax) == finite
