@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 4) act_fwd_kernel(const ActParams p)
     for (; row + (R - 1) * step < p.rows; row += R * step) body(std::integral_constant<int, R>{});
     for (; row < p.rows; row += step) body(std::integral_constant<int, 1>{});
   }
-  allow_next_launch();
+  if (threadIdx.x == 0) allow_next_launch();       // its column and first row are always there
   __syncwarp();
   amax.to(p.amax);
   if (!finite) set_status(p.status, FP4_ERR_NONFINITE, 7);
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, bwd_ctas(GATED, CKPT, DBIAS)) act_bw
     for (; row + (kRows - 1) * step < p.rows; row += kRows * step) body(std::integral_constant<int, kRows>{});
     for (; row < p.rows; row += step) body(std::integral_constant<int, 1>{});
   }
-  allow_next_launch();
+  if (threadIdx.x == 0) allow_next_launch();       // its column and first row are always there
   __syncwarp();
   amax.to(p.amax);
   if constexpr (DBIAS) {

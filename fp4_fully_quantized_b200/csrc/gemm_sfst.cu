@@ -416,6 +416,7 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(acc_empty);
+          if (tile + (int)gridDim.x >= num_tiles) allow_next_launch();   // only this epilogue is left
 #pragma unroll
           for (int i = 0; i < COLS; ++i) v[i] = __uint_as_float(r[i]);
         }
@@ -711,7 +712,6 @@ fp4_gemm_sfst_kernel(const __grid_constant__ CUtensorMap tmap_a,
     }
   }
 
-  if constexpr (EPI) allow_next_launch();
   tc_fence_before();
   __syncthreads();
   if (warp == MMA_WARP) {

@@ -85,7 +85,9 @@ cudaError_t launch_quant_2d(const Quant2DArgs& a, cudaStream_t s);
 // the stream ends: it touches no global memory before wait_previous_launch(),
 // which returns when that kernel (and with it all before it) has completed and
 // its writes are visible.  allow_next_launch(), once a CTA has little left to do,
-// lets the next such launch start.  In a stream of small calls the hand-over
+// lets the next such launch start when all CTAs have called it or ended.  A CTA's
+// first call counts, so threads without work leave it to the others: CTAs that
+// wait hold shared memory that another stream's kernels may need.  In a stream of small calls the hand-over
 // otherwise costs up to 2.5 us a kernel (a graph has it in the edge: 16.4 against
 // 13.8 us for a 128x4096x4096 fp4_gemm_epi), so captured launches are plain ones.
 __device__ __forceinline__ void wait_previous_launch() {

@@ -308,7 +308,7 @@ rmsnorm_fwd_kernel(const FwdParams p) {
     if (whole && (tile + 1) * at.rows_per_tile <= p.rows) body(tile, std::true_type{});
     else body(tile, std::false_type{});
   }
-  allow_next_launch();
+  if (tile0 < tiles) allow_next_launch();      // the CTA's first group always has a tile
   if (failed && at.first_warp) ring_give_up(ring, slot, phase, p.status, 0x4100);
   __syncwarp();
   amax.to(p.y_amax);
@@ -437,7 +437,7 @@ rmsnorm_bwd_kernel(const BwdParams p) {
     if (whole && (tile + 1) * at.rows_per_tile <= p.rows) body(tile, std::true_type{});
     else body(tile, std::false_type{});
   }
-  allow_next_launch();
+  if (tile0 < tiles) allow_next_launch();      // the CTA's first group always has a tile
   if (failed && at.first_warp) ring_give_up(ring, slot, phase, p.status, 0x4200);
   if (p.partial == nullptr) return;
   // join the CTA's rows through shared memory (no copies are on their way: every

@@ -147,3 +147,45 @@ def test_gemm_epi_amax_of_nonfinite_values(gpu_lib, m, n, out, kind):
     assert np.isnan(float(amax))
     F.fp4_gemm_epi(qa, qb, c, act=act, c_amax=amax)                # and the next call's is its own
     assert float(amax) == finite
+
+
+# --------------------------------------------------------------------------
+# Launches that start early, and another stream
+# --------------------------------------------------------------------------
+def test_early_launches_leave_room_for_another_stream(gpu_lib):
+    """A product of 32 narrow tiles with another one queued behind it leaves 116
+    SMs to a second stream: 110 tiles there run at once, as they do alone.  If
+    the queued product already held 32 SMs while it waits, they would take two
+    turns, twice the time."""
+    F = gpu_lib
+    k = 32768
+
+    def product(f, m, n):
+        qa, qb = _operands(F, m, n, k, 0)
+        c, ws = torch.zeros(m, n, device="cuda"), F.Workspace()
+        return lambda: f(qa, qb, c, ws=ws)
+
+    chain, other = product(F.fp4_gemm_epi, 128, 4096), product(F.fp4_gemm, 1280, 2816)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def time_other(beside):
+        times = []
+        for _ in range(5):
+            e0, e1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            torch.cuda.synchronize()
+            with torch.cuda.stream(a):
+                for _ in range(24 if beside else 0):
+                    chain()
+            with torch.cuda.stream(b):
+                other()                                   # the first, while the chain begins
+                e0.record()
+                for _ in range(8):
+                    other()
+                e1.record()
+            torch.cuda.synchronize()
+            times.append(e0.elapsed_time(e1))
+        return sorted(times)[2]
+
+    time_other(True)
+    alone, beside = time_other(False), time_other(True)
+    assert beside < 1.4 * alone, (beside, alone)
