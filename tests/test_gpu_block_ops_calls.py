@@ -189,3 +189,108 @@ def test_early_launches_leave_room_for_another_stream(gpu_lib):
     time_other(True)
     alone, beside = time_other(False), time_other(True)
     assert beside < 1.4 * alone, (beside, alone)
+
+
+# --------------------------------------------------------------------------
+# RMS norm: every pair of stored and gradient type, without the residual's
+# gradient; rings that go round
+# --------------------------------------------------------------------------
+def _within(got, want, bound, what):
+    off = (got.double() - want).abs()
+    bad = ~(off <= bound)
+    assert not bool(bad.any()), (what, int(bad.sum()), bad.nonzero()[0].tolist(), float(off[bad].max()))
+
+
+def _bwd_case(F, rows, cols, saved, grad, dres, seed):
+    """One backward against the formulas in 64 bits; the bounds are those of
+    test_gpu_block_ops.test_rmsnorm_bwd."""
+    s = rand(rows, cols, seed=seed, dtype=TYPES["f32" if saved == "f32" else "bf16"])
+    s[:, : max(1, cols // 50)] *= 20
+    rstd = torch.rsqrt(s.float().square().mean(1) + 1e-5)
+    w = rand(cols, seed=seed + 1, std=0.2, mean=1.0, dtype=F32)
+    dy = rand(rows, cols, seed=seed + 2, std=0.1)
+    dr = rand(rows, cols, seed=seed + 3, std=0.1, dtype=TYPES[grad]) if dres else None
+    if saved == "ckpt":
+        q8 = F.Ckpt8.empty(rows, cols)
+        F.fqt_act_fwd((s.float() * rstd[:, None]).to(BF16), act=F.ACT_NONE, z8=q8)
+        e = torch.ldexp(torch.ones_like(q8.scales, dtype=torch.float64), q8.scales.int() - 127)
+        kw, xhat = {"xhat8": q8}, q8.codes.view(torch.float8_e4m3fn).double() * e.repeat_interleave(32, 1)
+    else:
+        kw, xhat = {"s": s}, s.double() * rstd.double()[:, None]
+    dx, dw = torch.full((rows, cols), 7.0, dtype=TYPES[grad], device="cuda"), torch.full((cols,), 5.0, device="cuda")
+    F.fqt_rmsnorm_bwd(dy, w, rstd, dx, dres=dr, dweight=dw, **kw)
+    r, d = rstd.double()[:, None], dy.double()
+    t, g = d * xhat, d * w.double()
+    gx = g * xhat
+    m, ma = gx.mean(1, keepdim=True), gx.abs().mean(1, keepdim=True)
+    want = r * (g - xhat * m) + (dr.double() if dres else 0)
+    bound = EPS32 * (8 * r * (g.abs() + xhat.abs() * m.abs()) + 72 * r * xhat.abs() * ma +
+                     (2 * dr.double().abs() if dres else 0)) + STEP[TYPES[grad]] * want.abs() * 1.01 + TINY
+    _within(dx, want, bound, "dx")
+    chain = rows / 148 + 2 + 32 + 14 + 32
+    _within(dw, t.sum(0), EPS32 * chain * t.abs().sum(0) + TINY, "dweight")
+    alone = torch.zeros_like(dx)
+    F.fqt_rmsnorm_bwd(dy, w, rstd, alone, dres=dr, **kw)              # without dweight
+    assert torch.equal(alone, dx)
+
+
+NORM_SHAPES = [(1, 8), (3, 64), (5, 72), (33, 256), (9, 264), (17, 1000), (9, 1024), (300, 1056), (401, 4096),
+               (2, 4104), (500, 8200), (350, 16384), (1201, 96), (5000, 2056), (9000, 64)]
+
+
+@pytest.mark.parametrize("rows,cols", NORM_SHAPES)
+@pytest.mark.parametrize("saved", ["bf16", "f32"])
+@pytest.mark.parametrize("grad", ["bf16", "f32"])
+@pytest.mark.parametrize("dres", [False, True])
+def test_rmsnorm_bwd_from_the_stored_sum(gpu_lib, rows, cols, saved, grad, dres):
+    _bwd_case(gpu_lib, rows, cols, saved, grad, dres, seed=60)
+
+
+def _rows_round(cols, bytes_per_value):
+    """Rows of more than twice all the shared memory of 148 SMs, so that every
+    group of threads goes round its ring more than twice; rings of short rows
+    have at most 8 stages of 32 rows in each of 444 CTAs."""
+    return min(int(2.2 * 148 * 228 * 1024 / (cols * bytes_per_value)), int(2.2 * 444 * 8 * 32)) + 13
+
+
+# one width for each of the layouts: 8 and 16 threads to a row with one to four
+# chunks, 32, and more, some a multiple of the threads' columns and some not
+RING_COLS = [64, 128, 192, 256, 352, 512, 544, 768, 1024, 1440, 2080, 2336, 2784, 4096, 4128, 5344, 6880, 8192,
+             8224, 9696, 12288, 14496, 16384]
+
+
+@pytest.mark.parametrize("cols", RING_COLS)
+@pytest.mark.parametrize("saved,grad,dres,value_bytes", [
+    ("bf16", "bf16", False, 4), ("bf16", "bf16", True, 6), ("f32", "bf16", True, 8), ("f32", "f32", True, 10),
+    ("ckpt", "bf16", False, 3), ("ckpt", "bf16", True, 5), ("ckpt", "f32", True, 7)])
+def test_rmsnorm_bwd_rings_go_round(gpu_lib, cols, saved, grad, dres, value_bytes):
+    _bwd_case(gpu_lib, _rows_round(cols, value_bytes), cols, saved, grad, dres, seed=70)
+
+
+@pytest.mark.parametrize("cols", RING_COLS)
+@pytest.mark.parametrize("residual,q8,value_bytes", [(None, False, 2), (None, True, 2), ("bf16", False, 4),
+                                                     ("bf16", True, 4), ("f32", True, 6)])
+def test_rmsnorm_fwd_rings_go_round(gpu_lib, cols, residual, q8, value_bytes):
+    """The bounds are those of test_gpu_block_ops.test_rmsnorm_fwd."""
+    F, rows = gpu_lib, _rows_round(cols, value_bytes)
+    x, r, w = _norm_inputs(rows, cols, residual, "f32", seed=80)
+    y, rstd = torch.zeros_like(x), torch.zeros(rows, device="cuda")
+    res = torch.zeros_like(r) if residual else None
+    q = F.Ckpt8.empty(rows, cols) if q8 else None
+    F.fqt_rmsnorm_fwd(x, w, y, residual=r, res_out=res, q8=q, q8_of=F.RMS_XHAT, rstd=rstd, eps=1e-5)
+    s = x.double() + r.double() if residual else x.double()
+    rs = (s.square().mean(1) + 1e-5).rsqrt()
+    _within(rstd, rs, 48 * EPS32 * rs, "rstd")
+    if residual:
+        assert torch.equal(res, (x.float() + r.float()).to(r.dtype))
+    xhat = s * rs[:, None]
+    want = xhat * w.double()
+    _within(y, want, want.abs() * (EPS16 + 56 * EPS32) + TINY, "y")
+    if q8:
+        e = torch.ldexp(torch.ones_like(q.scales, dtype=torch.float64), q.scales.int() - 127).repeat_interleave(32, 1)
+        top = xhat.abs().view(rows, -1, 32).amax(2)
+        assert bool((top * (1 - 56 * EPS32) <= 448 * e[:, ::32]).all())
+        assert bool((top * (1 + 56 * EPS32) > 224 * e[:, ::32]).all())       # the least such power
+        values = q.codes.view(torch.float8_e4m3fn).double() * e
+        _within(values, xhat, torch.maximum(xhat.abs() * 2.0 ** -4, e * 2.0 ** -10) * (1 + 2.0 ** -10) +
+                xhat.abs() * 56 * EPS32, "checkpoint")
