@@ -282,11 +282,13 @@ cudaError_t launch(ActParams& p, int act, bool gated, unsigned& slices, cudaStre
   }
 }
 
-// The checks that both directions make of their shape and of z.
-fp4_status check_act(const void* z, int64_t ldz, const fqt_ckpt8* z8, int32_t act, int64_t rows,
-                     int64_t cols, int64_t zcols, const void* ws, size_t ws_bytes) {
+// The checks that both directions make of their shape and of z; z's row length.
+constexpr int64_t kMaxZCols = (int64_t)1 << 30;
+fp4_status check_act(const void* z, int64_t ldz, const fqt_ckpt8* z8, int32_t act, int32_t gated,
+                     int64_t rows, int64_t cols, const void* ws, size_t ws_bytes, int64_t& zcols) {
   if (!known_act(act)) return FP4_ERR_FORMAT;
-  if (rows < 0 || cols <= 0 || cols % 8 || zcols > ((int64_t)1 << 30)) return FP4_ERR_SHAPE;
+  if (rows < 0 || cols <= 0 || cols % 8 || cols > (gated ? kMaxZCols / 2 : kMaxZCols)) return FP4_ERR_SHAPE;
+  zcols = gated ? 2 * cols : cols;
   if (ws != nullptr && ws_bytes < sizeof(DeviceStatus)) return FP4_ERR_WORKSPACE;
   if (z8 != nullptr) {
     if (z != nullptr) return FP4_ERR_FORMAT;
@@ -306,8 +308,8 @@ extern "C" {
 fp4_status fqt_act_fwd(const fqt_act_fwd_args* args, void* ws, size_t ws_bytes, void* stream) {
   if (args == nullptr) return FP4_ERR_NULL;
   const auto& [z, ldz, z8_in, y, ldy, z8_out, y_amax, rows, cols, act, gated] = *args;
-  const int64_t zcols = gated ? 2 * cols : cols;
-  fp4_status st = check_act(z, ldz, z8_in, act, rows, cols, zcols, ws, ws_bytes);
+  int64_t zcols = 0;
+  fp4_status st = check_act(z, ldz, z8_in, act, gated, rows, cols, ws, ws_bytes, zcols);
   if (st != FP4_OK) return st;
   if (rows > 0 && y == nullptr && (z8_out == nullptr || y_amax != nullptr)) return FP4_ERR_NULL;
   if (z8_in != nullptr && z8_out != nullptr) return FP4_ERR_FORMAT;
@@ -334,8 +336,8 @@ fp4_status fqt_act_fwd(const fqt_act_fwd_args* args, void* ws, size_t ws_bytes, 
 fp4_status fqt_act_bwd(const fqt_act_bwd_args* args, void* ws, size_t ws_bytes, void* stream) {
   if (args == nullptr) return FP4_ERR_NULL;
   const auto& [dy, lddy, z, ldz, z8, dz, lddz, dbias, dz_amax, rows, cols, act, gated] = *args;
-  const int64_t zcols = gated ? 2 * cols : cols;
-  fp4_status st = check_act(z, ldz, z8, act, rows, cols, zcols, ws, ws_bytes);
+  int64_t zcols = 0;
+  fp4_status st = check_act(z, ldz, z8, act, gated, rows, cols, ws, ws_bytes, zcols);
   if (st != FP4_OK) return st;
   if (rows > 0 && ((st = check_matrix(dy, cols, lddy)) != FP4_OK ||
                    (st = check_matrix(dz, zcols, lddz)) != FP4_OK))

@@ -444,9 +444,10 @@ fp4_status fqt_rmsnorm_bwd(const fqt_rmsnorm_bwd_args* args, void* ws, size_t ws
                            void* stream);
 
 /* Activation forward.  gated == 0: y = act(z), z [rows, cols]; gated != 0:
- * y = act(z[:, :cols]) * z[:, cols:], z [rows, 2 cols].  z comes as BF16 (`z`,
- * leading dimension ldz) or from a checkpoint (`z8_in`: the recomputation of
- * y; with FQT_ACT_NONE the checkpoint's decoding): exactly one of the two.
+ * y = act(z[:, :cols]) * z[:, cols:], z [rows, 2 cols].  A row of z has at most
+ * 2^30 values.  z comes as BF16 (`z`, leading dimension ldz) or from a
+ * checkpoint (`z8_in`: the recomputation of y; with FQT_ACT_NONE the
+ * checkpoint's decoding): exactly one of the two.
  * Outputs: y BF16 [rows, cols]; z8_out the checkpoint of a BF16 z (with y
  * NULL: encoding alone); y_amax.  y or z8_out is needed, y_amax needs y. */
 typedef struct fqt_act_fwd_args {

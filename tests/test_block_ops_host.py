@@ -238,3 +238,12 @@ def test_binding_checks_tensors(lib):
     for o in [dict(dz=y[:2]), dict(z=x[:, :32]), dict(dbias=torch.zeros(32)), dict(gated=True)]:
         with pytest.raises(ValueError):
             F.fqt_act_bwd(**{**dict(dy=x, z=x, dz=y), **o})
+
+
+@pytest.mark.parametrize("cols", [1 << 62, (1 << 62) + 64, (1 << 29) + 32, (1 << 63) - 64])
+def test_row_lengths_past_the_limit_are_refused(lib, cols):
+    """Twice a row length beyond 2^62 is not a 64-bit number."""
+    wide = dict(cols=cols, ldz=(1 << 63) - 8, ldy=(1 << 63) - 8)
+    assert _afwd(lib, **wide) == SHAPE and _afwd(lib, **wide, zo=_ck(4, -(1 << 63))) == SHAPE
+    wide = dict(cols=cols, ldz=(1 << 63) - 8, lddy=(1 << 63) - 8, lddz=(1 << 63) - 8)
+    assert _abwd(lib, **wide) == SHAPE
