@@ -107,8 +107,11 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
 // gelu(z) = z Phi(z) with the normal CDF Phi; gelu_tanh(z) = z (1 + tanh u) / 2 =
 // z p(2u), u = sqrt(2/pi) (z + 0.044715 z^3).  Exponential and reciprocal are the
 // hardware's approximations (2 and 1 units in the last place, subnormals
-// flushed), against 2^-9 of a BF16 result.  z^2 is capped in gelu_tanh where p
-// is 0 or 1 in binary32 anyway, so that a large z does not meet Inf * 0.
+// flushed).  With the roundings of the arguments a value is within (|t| + 4) 2^-20
+// of itself (t = z or 2u), GELU within 2^-20 |z| and, left of zero, 2^-10 of
+// itself: a quarter of a BF16 half-step or less, but some 16 (|t| + 4) half-steps
+// of FP32, which the GEMM's epilogue may store.  z^2 is capped in gelu_tanh where
+// p is 0 or 1 in binary32 anyway, so that a large z does not meet Inf * 0.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float ex2_approx(float x) {
   float r;
@@ -142,23 +145,33 @@ __device__ __forceinline__ f32x2 logistic2(f32x2 t) {
   return pair(rcp_approx(d.x), rcp_approx(d.y));
 }
 
+// 1 for v >= 0, else 0, in one instruction.
+__device__ __forceinline__ float step(float v) {
+  float r;
+  asm("set.ge.f32.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // Minus the upper normal tail, -Q(a) = Phi(a) - 1, and e = exp(-a^2/2) at
-// a = min(|z|, 14), by the rational approximation of erfc of Abramowitz and
-// Stegun, Handbook of Mathematical Functions, 7.1.26: for x >= 0 erfc(x) =
-// (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), to 1.5e-7, with
-// x = a / sqrt(2): the exponential is the density's too.  An error of 0.75e-7 is
-// one and a quarter units of FP32's last place at 1.
+// a = min(|z|, 14): Q(a) = p(t) e with t = 1 / (1 + 0.33 a), the form that
+// Hastings gave such approximations (Abramowitz and Stegun, 7.1.26, is one), and p
+// of degree five with a constant term.  Its coefficients are a weighted minimax
+// fit of exp(a^2/2) Q(a) on [0, 14] (a linear program): within 0.98e-7 of Q, 1.6
+// units of FP32's last place at 1, and within 2^-10 of Q relative to
+// it, where 7.1.26 itself (0.75e-7) is off by 0.16 % at a = 5, 1 % at 8 and 4 %
+// at 14.  In FP32 arithmetic 2.4e-7.  e is the density's exponential too.
 __device__ __forceinline__ void normal_tail2(float2 z, f32x2& a, f32x2& nq, f32x2& e) {
   a = pair(min_nan(fabsf(z.x), 14.0f), min_nan(fabsf(z.y), 14.0f));
-  const float2 d = unpair(fma2(a, both(0.23164190f), both(1.0f)));      // 0.3275911 / sqrt(2)
+  const float2 d = unpair(fma2(a, both(0.33f), both(1.0f)));
   const f32x2 t = pair(rcp_approx(d.x), rcp_approx(d.y));
   const float2 x = unpair(mul2(mul2(a, both(-0.5f * kLog2e)), a));
   e = pair(ex2_approx(x.x), ex2_approx(x.y));
-  f32x2 q = fma2(t, both(-0.5f * 1.061405429f), both(0.5f * 1.453152027f));
-  q = fma2(q, t, both(-0.5f * 1.421413741f));
-  q = fma2(q, t, both(0.5f * 0.284496736f));
-  q = fma2(q, t, both(-0.5f * 0.254829592f));
-  nq = mul2(mul2(q, t), e);
+  f32x2 q = fma2(t, both(0.115314774f), both(-0.398171842f));
+  q = fma2(q, t, both(0.126772538f));
+  q = fma2(q, t, both(-0.230730325f));
+  q = fma2(q, t, both(-0.111643821f));
+  q = fma2(q, t, both(-0.00154125539f));
+  nq = mul2(q, e);
 }
 
 // act(z)
@@ -196,13 +209,13 @@ __device__ __forceinline__ void act_both2(f32x2 z, f32x2& f, f32x2& df) {
     df = fma2(f, fma2(p, both(-1.0f), both(1.0f)), p);
   }
   if constexpr (ACT == FQT_ACT_GELU) {
-    // Phi + z phi = 1/2 +- (1/2 - Q) + z phi: beyond |z| = 14 the last is below 2^-126
+    // Phi + z phi: 1 + (|z| phi - Q) right of zero, -(|z| phi - Q) left of it;
+    // beyond |z| = 14 both are below 2^-126
     f32x2 a, nq, e;
     normal_tail2(v, a, nq, e);
     f = fma2(a, nq, pair(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
-    const f32x2 odd = fma2(mul2(a, both(0.3989422804014327f)), e, add2(nq, both(0.5f)));
-    const float2 o = unpair(odd);
-    df = add2(pair(copysignf(o.x, v.x), copysignf(o.y, v.y)), both(0.5f));
+    const f32x2 right = pair(step(v.x), step(v.y));
+    df = fma2(fma2(mul2(a, both(0.3989422804014327f)), e, nq), fma2(right, both(2.0f), both(-1.0f)), right);
   }
   if constexpr (ACT == FQT_ACT_GELU_TANH) {
     const float2 s = unpair(mul2(z, z));

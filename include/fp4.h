@@ -449,7 +449,11 @@ fp4_status fqt_rmsnorm_bwd(const fqt_rmsnorm_bwd_args* args, void* ws, size_t ws
  * checkpoint (`z8_in`: the recomputation of y; with FQT_ACT_NONE the
  * checkpoint's decoding): exactly one of the two.
  * Outputs: y BF16 [rows, cols]; z8_out the checkpoint of a BF16 z (with y
- * NULL: encoding alone); y_amax.  y or z8_out is needed, y_amax needs y. */
+ * NULL: encoding alone); y_amax.  y or z8_out is needed, y_amax needs y.
+ * Before y is rounded, SiLU is within (|z| + 4) 2^-20 of its value, GELU_TANH
+ * within (|2u| + 4) 2^-20, u = sqrt(2/pi) (z + 0.044715 z^3), and GELU within
+ * 2^-20 |z| and, for z < 0, 2^-10 of its value; what is below 2^-126 |z| may be
+ * zero. */
 typedef struct fqt_act_fwd_args {
   const void* z;              /* BF16 [rows, ldz], or NULL              */
   int64_t ldz;

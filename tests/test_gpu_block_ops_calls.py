@@ -294,3 +294,49 @@ def test_rmsnorm_fwd_rings_go_round(gpu_lib, cols, residual, q8, value_bytes):
         values = q.codes.view(torch.float8_e4m3fn).double() * e
         _within(values, xhat, torch.maximum(xhat.abs() * 2.0 ** -4, e * 2.0 ** -10) * (1 + 2.0 ** -10) +
                 xhat.abs() * 56 * EPS32, "checkpoint")
+
+
+# --------------------------------------------------------------------------
+# GELU's left tail, where the value is small against z
+# --------------------------------------------------------------------------
+def _all_bf16(lo, hi):
+    """Every BF16 value in [lo, hi], a row of them."""
+    v = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(BF16).float()
+    v = v[(v >= lo) & (v <= hi)]
+    return v[: v.numel() // 32 * 32].to(BF16).cuda().view(1, -1)
+
+
+def _upper_tail(a):
+    """1 - Phi(a); torch's ndtr is a sum with 1, which leaves 2^-53 of error."""
+    return torch.special.erfc(a * 0.5 ** 0.5) / 2
+
+
+def test_gelu_tail(gpu_lib):
+    """Relative to the value itself, for z < 0.  The tail function Q is within
+    2^-10 (a fit within 0.85 * 2^-10, act_device.cuh; the exponent, up to 141,
+    has three roundings of 2^-24, 1.7e-5, and the rest is below that), the
+    result is rounded once; where exp(-z^2 / 2) is below FP32's normal range it
+    may be flushed to zero: |z| 2^-126.  The derivative is Q - |z| phi, phi
+    within 2^-15 by the same exponent."""
+    F = gpu_lib
+    z = _all_bf16(-40.0, -2.0 ** -20)
+    y, dz, one = torch.zeros_like(z), torch.zeros_like(z), torch.ones_like(z)
+    F.fqt_act_fwd(z, y, act=F.ACT_GELU)
+    F.fqt_act_bwd(one, z, dz, act=F.ACT_GELU)
+    a = -z.double()
+    q, pdf = _upper_tail(a), torch.exp(-a * a / 2) / (2 * np.pi) ** 0.5
+    flush = (1 + a) * 2.0 ** -126
+    _within(y, -a * q, a * q * (EPS16 + 2.0 ** -10) + flush, "gelu")
+    _within(dz, q - a * pdf, (q - a * pdf).abs() * EPS16 + q * 2.0 ** -10 + a * pdf * 2.0 ** -15 + flush, "derivative")
+
+
+def test_gemm_epi_gelu_tail(gpu_lib):
+    """The same of an FP32 output: z is what the product and bias give exactly."""
+    F = gpu_lib
+    qa, qb = _operands(F, 128, 256, 64, 0)
+    zero = torch.zeros(128, 256, device="cuda")
+    bias = -torch.linspace(0.01, 12.5, 256, device="cuda")
+    F.fp4_gemm_epi(qa, qb, zero, alpha=0.0, bias=bias, act=F.ACT_GELU)
+    a = -bias.double()
+    q = _upper_tail(a)
+    _within(zero, (-a * q).expand(128, 256), (a * q * 2.0 ** -10).expand(128, 256), "gelu")
