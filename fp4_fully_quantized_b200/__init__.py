@@ -463,13 +463,18 @@ class Ckpt8:
     cols: int
     codes: torch.Tensor
     scales: torch.Tensor
-    # the C structure that the last call got, its address and (_at) what it says:
-    # _ckpt makes another when that is no longer so
+    # the C structure that calls get, its address, and (_at) what it was checked and
+    # made for: see _ckpt
     _c: Ckpt8C = field(default=None, repr=False, compare=False)
     _address: int = field(default=0, repr=False, compare=False)
 
     def __post_init__(self):
-        self._c, self._address, self._at = None, 0, None      # none yet, or another object's
+        self._c, self._address = None, 0              # none yet, or another object's
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name in ("rows", "cols", "codes", "scales"):
+            object.__setattr__(self, "_at", None)
 
     def __reduce__(self):
         return Ckpt8, (self.rows, self.cols, self.codes, self.scales)
@@ -540,14 +545,19 @@ def _ckpt(where, name, q, rows, cols, dev):
     """Address of a checkpoint's structure, 0 for None."""
     if q is None:
         return 0
-    if not isinstance(q, Ckpt8) or q.rows != rows or q.cols != cols:
+    if not isinstance(q, Ckpt8):
+        _bad(where, name, q, "a Ckpt8")
+    # checked before, nothing assigned since, and the memory where it was
+    if q._at is not None and q._at == (q.codes.data_ptr(), q.scales.data_ptr(), rows, cols, dev):
+        return q._address
+    if q.rows != rows or q.cols != cols:
         _bad(where, name, q, f"a Ckpt8 of [{rows}, {cols}]")
     _bytes(where, name, "codes", q.codes, rows, cols, torch.float8_e4m3fn, dev)
     _bytes(where, name, "scales", q.scales, rows, cols // 32, torch.float8_e8m0fnu, dev)
-    at = (q.codes.data_ptr(), q.scales.data_ptr(), rows, cols)
-    if q._at != at:
-        q._c = Ckpt8C(*at)
-        q._address, q._at = C.addressof(q._c), at
+    at = (q.codes.data_ptr(), q.scales.data_ptr(), rows, cols, dev)
+    q._c = Ckpt8C(*at[:4])
+    q._address = C.addressof(q._c)
+    q._at = at
     return q._address
 
 
@@ -657,9 +667,11 @@ def fqt_act_fwd(z, y: torch.Tensor | None = None, act: int = ACT_SILU, gated: bo
     me = "fqt_act_fwd"
     zp = ldz = zc = yp = ldy = 0
     src = z.codes if isinstance(z, Ckpt8) else z
-    if not isinstance(src, torch.Tensor) or src.dim() != 2 or (gated and src.shape[1] % 2):
-        _bad(me, "z", src, "a matrix, with an even row length when gated")
+    if src is not z and not isinstance(src, torch.Tensor):
+        _bad(me, "z.codes", src, "a tensor")
     dev, zshape = src.get_device(), src.shape
+    if len(zshape) != 2 or (gated and zshape[1] % 2):
+        _bad(me, "z", src, "a matrix, with an even row length when gated")
     rows, zcols = zshape
     cols = zcols // 2 if gated else zcols
     if src is z:
