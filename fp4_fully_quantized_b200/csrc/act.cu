@@ -71,7 +71,8 @@ struct Stored<true> {
 
 // Rows whose loads are in flight together: about 40 KB an SM cover the memory's
 // latency, and a row of a checkpoint is half a row of BF16 (recomputing ReLU with
-// two rows: 0.77 of the copy rate).
+// two rows: 0.77 of the copy rate, with four 0.90; gated, four spill up to 12 bytes
+// in the activations other than GELU).
 constexpr int kRows = 2, kCkptFwdRows = 4;
 
 template <int ACT, bool GATED, bool CKPT>
@@ -135,10 +136,14 @@ __global__ void __launch_bounds__(kThreads, 4) act_fwd_kernel(const ActParams p)
   if (!finite) set_status(p.status, FP4_ERR_NONFINITE, 7);
 }
 
-// The backward's CTAs to an SM: as many as have registers for two rows each
-// without spills (16384x8192 SwiGLU from a checkpoint: 0.90 of the copy rate with
+// The backward's CTAs to an SM: as many as have registers for two rows each with
+// no spills for SwiGLU (16384x8192 from a checkpoint: 0.90 of the copy rate with
 // three, 0.89 with four, 0.86 with five of one row; with dbias from BF16 0.90 with
-// two, 0.83 with three).
+// two, 0.83 with three).  The rule does not look at the activation: without dbias
+// others spill a few bytes (-Xptxas -v: gated GELU_TANH from BF16 24 stored and 36
+// loaded, at most 12 elsewhere), and SiLU with dbias, not gated, from BF16 8 and 12.
+// They run at 0.96 (that GELU_TANH), 0.90-0.92 (gated GELU and ReLU from BF16, ReLU
+// from a checkpoint) and 0.89 of the copy rate at 16384x8192.
 constexpr int bwd_ctas(bool gated, bool ckpt, bool dbias) { return gated && dbias ? 2 : gated && ckpt ? 3 : 4; }
 
 template <int ACT, bool GATED, bool CKPT, bool DBIAS>
@@ -234,7 +239,8 @@ int lanes_for(int64_t cols) { return cols <= 64 ? 8 : cols <= 128 ? 16 : 32; }
 // the fewest (of up to 64, and no more than there are groups of rows) that fill
 // their waves to 0.96, else those that fill them best; a CTA then has many rows,
 // and there are few partial sums.  148 is a constant here, so that
-// sums do not depend on the device.
+// sums do not depend on the device.  The limit of kMaxSlices, which the partial
+// sums have, holds for all calls: where one CTA covers the width, three fit an SM.
 dim3 act_grid(int64_t rows, int64_t cols, int lanes, int per_sm) {
   const int64_t wave = 148 * per_sm;
   const int64_t gx = (cols + lanes * 8 - 1) / (lanes * 8);

@@ -120,7 +120,8 @@ cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, int threads,
 // --- sums over rows (colsum.cu) ----------------------------------------------
 // Kernels that sum over rows (dweight, dbias) write one partial row of sums per
 // row slice behind the status block of the workspace; launch_colsum adds the
-// slices in order, so a result's additions depend on the shape alone.
+// slices in order, so a result's additions depend on the call's shape, types and
+// optional arguments alone (the rows of a slice follow from what a CTA holds).
 constexpr int kMaxSlices = 444;      // three CTAs on each of 148 SMs
 inline int64_t colsum_slices(int64_t rows) { return rows < kMaxSlices ? rows : kMaxSlices; }
 inline float* colsum_partials(void* ws) {

@@ -316,7 +316,10 @@ rmsnorm_fwd_kernel(const FwdParams p) {
 }
 
 // SRC: 0 the stored sum in BF16, 1 in FP32, 2 the 8-bit checkpoint of xhat.
-// GF32: dres and dx in FP32.
+// GF32: dres and dx in FP32.  Of the forms with four chunks the FP32 sum with BF16
+// gradients spills (48 bytes stored, 92 loaded; 32768x4096 with dres 252 us, 0.81
+// of the copy rate, against 303 us, 0.95, with FP32 gradients), the checkpoint with
+// BF16 ones 8 bytes.
 template <int W, int V, int SRC, bool GF32, int THREADS>
 __global__ void __launch_bounds__(THREADS, V <= 2 ? 3 : 512 / THREADS)
 rmsnorm_bwd_kernel(const BwdParams p) {
@@ -465,10 +468,13 @@ rmsnorm_bwd_kernel(const BwdParams p) {
 // as one CTA (one stage, in the backward of 8192 columns: 0.67 of the copy rate
 // against 0.85).  A forward that moves nine bytes a value or more gets 256
 // threads: fewer rows at a time are in flight then, and the memory's mix of reads
-// and writes runs better (32768x4096 with an FP32 residual and a checkpoint, 13
-// bytes: 0.95 of the copy rate against 0.86; 16384x8192, 9 bytes: 0.95 against
-// 0.84); below, 256 threads do not issue fast enough (4 bytes: 0.69 against 0.94;
-// 8 bytes: 0.86 against 0.88).  Short rows (two chunks a thread at most, 80
+// and writes mostly runs better.  Both sides in turn on one GPU, shares of the copy
+// rate at 134 million values, rows of 512, 1024, 2048, 4096 and 8192: BF16 residual
+// and checkpoint (9 bytes) 0.97, 0.93, 0.87, 0.84, 0.86 against 0.85, 0.84, 0.84,
+// 0.83, 0.83; FP32 residual (12) 0.84, 0.84, 0.85, 0.87, 0.99 against 0.86, 0.88,
+// 0.81, 0.83, 0.87; with a checkpoint too (13) 0.85-0.86 against 0.85-0.87.  Below
+// nine, 256 threads do not issue fast enough (4 bytes: 0.69 against 0.94; 8 bytes:
+// 0.86 against 0.88).  Short rows (two chunks a thread at most, 80
 // registers) run three CTAs of 256 threads (40001x128: 7.4 us against 8.1 with two).
 struct RowPlan { int T, chunks, threads, rows_per_cta, stages, smem, per_sm; };
 RowPlan row_plan(int64_t cols, int bytes_per_value, bool row_sums, bool few) {

@@ -343,11 +343,12 @@ fp4_status fp4_quant_noise(const void* x_bf16, int64_t rows, int64_t cols, int64
 /* number of rows from 0 on.  Sums, statistics and every intermediate are    */
 /* FP32; each output is rounded once.  An output may be the input that its   */
 /* comment names, with the same leading dimension and type; no other buffers */
-/* may overlap.  Results do not depend on the launch configuration, except   */
-/* that column sums over rows are added in an order fixed by the shape       */
-/* alone.  `ws` may be NULL where no workspace size is asked for (device     */
-/* conditions are then not recorded); calls that may run at the same time,   */
-/* replays of captured graphs among them, need workspaces of their own.      */
+/* may overlap.  The same call gives the same bits every time; the order in  */
+/* which column sums over rows are added follows from the shape, the types   */
+/* and which arguments are given, not from the device.  `ws` may be NULL     */
+/* where no workspace size is asked for (device conditions are then not      */
+/* recorded); calls that may run at the same time, replays of captured       */
+/* graphs among them, need workspaces of their own.                          */
 /* y_amax and dz_amax are max |v| of the values as stored in BF16, so that    */
 /* fp4_quantize with that amax_in gives the bits that it gives with its own   */
 /* amax pass; fp4_gemm_epi's c_amax is of its FP32 values.  A NaN or Inf      */
@@ -474,7 +475,8 @@ fp4_status fqt_act_fwd(const fqt_act_fwd_args* args, void* ws, size_t ws_bytes, 
  * dy * act(z[:, :cols])] when gated; z as above.  dy BF16 [rows, cols]; dz
  * BF16 of z's shape (may be z, or dy when not gated); dbias (nullable) FP32
  * [z's row length], overwritten with the sums of the unrounded dz over the
- * rows; dz_amax nullable.  act' of ReLU at 0 is 0.  With dbias, ws must hold
+ * rows; dz_amax nullable.  act' of ReLU at 0 is 0.  The gradient of a bias that
+ * no activation follows: FQT_ACT_NONE with dy as z and as dz.  With dbias, ws must hold
  * fqt_colsum_workspace_bytes(rows, z's row length). */
 typedef struct fqt_act_bwd_args {
   const void* dy;             /* BF16 [rows, lddy]                      */

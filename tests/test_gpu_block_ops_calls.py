@@ -340,3 +340,21 @@ def test_gemm_epi_gelu_tail(gpu_lib):
     a = -bias.double()
     q = _upper_tail(a)
     _within(zero, (-a * q).expand(128, 256), (a * q * 2.0 ** -10).expand(128, 256), "gelu")
+
+
+# --------------------------------------------------------------------------
+# The gradient of a bias that no activation follows
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("rows,cols", [(1, 8), (33, 72), (260, 4096), (4099, 264)])
+def test_bias_gradient_without_activation(gpu_lib, rows, cols):
+    """ACT_NONE with dy as z and dz: the sums of dy over the rows, dy as it was,
+    the padding of its rows too."""
+    F = gpu_lib
+    dy = rand(rows, cols, seed=1, std=0.1)
+    buf, a = padded(dy, 24)
+    db = torch.full((cols,), 5.0, device="cuda")
+    F.fqt_act_bwd(a, a, a, act=F.ACT_NONE, dbias=db, ws=F.Workspace.colsum(rows, cols))
+    assert torch.equal(a, dy) and (buf[:, cols:] == 7.0).all()
+    d = dy.double()
+    # chains: rows of a thread, 32 rows of the CTA, 14 and 32 slices
+    _within(db, d.sum(0), EPS32 * (rows / 4 + 32 + 14 + 32) * d.abs().sum(0) + TINY, "dbias")
